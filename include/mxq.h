@@ -379,6 +379,116 @@ MXQ_API mxq_status mxq_attention_mxfp4(const void* q_codes, const void* q_sf, co
                                        mxq_stream_t stream);
 
 /*
+ * Queries and keys on their way to the attention, and a paged cache.
+ *
+ * mxq_norm_rope -- the norm and the rotation of queries and keys.  With x the values of one
+ * head (span HEAD) or of the whole row of heads (span ROW), in FP32:
+ *   y = w * x / sqrt(mean(x^2) + eps)         (an operand whose weight is NULL: y = x)
+ *   (y_a, y_b) = (y_a c_i - y_b s_i, y_b c_i + y_a s_i)  for i < rot / 2 of each head, with
+ *   (a, b) = (i, i + rot / 2) (HALVES) or (2 i, 2 i + 1) (PAIRS),
+ *   c_i = table[position][i], s_i = table[position][rot / 2 + i];
+ * values from `rot` on are not rotated.  q_weight / k_weight: device BF16 [d] (HEAD) or
+ * [heads * d] (ROW), 16-byte aligned.  table: device FP32 [table_rows][rot], 16-byte aligned,
+ * or NULL with rot = 0 (no rotation).  d: a multiple of 16 up to 256; rot: a multiple of 16 up
+ * to d.  The structs of this section are read during the call only.
+ *
+ * mxq_paged_kv -- a cache of num_pages pages of page_size tokens of `heads` key heads of d
+ * values: the value i of head h of token t of page g is at element g * stride_page + t *
+ * stride_token + h * stride_head + i of k and v (so [page][token][head][d], [page][head][token][d]
+ * and pages interleaved with something else are all one case).  Elements: BF16 (scales 1), or
+ * E4M3 bytes whose values are times k_scale / v_scale, finite and positive.  k, v 16-byte aligned,
+ * strides multiples of 16 bytes and at least d; page_size a multiple of 8; heads * d <= 2^16.
+ *
+ * mxq_paged_batch -- `batch` sequences (up to 2^20): the rows [cu_q[b], cu_q[b + 1]) of Q, K, V are sequence b's
+ * new tokens (cu_q[0] = 0, non-decreasing; none is fine; rows from cu_q[batch] on belong to no
+ * sequence), kv_len[b] its length with them, and block_table[b][i] the page of its positions
+ * [i * page_size, (i + 1) * page_size).  New token i of n has position kv_len[b] - n + i.  All
+ * device int32; max_pages * page_size <= 2^30.  Table entries outside [0, num_pages) are
+ * pages that are missing: nothing is stored there, and their positions are not attended.
+ */
+typedef enum { MXQ_NORM_HEAD = 0, MXQ_NORM_ROW = 1 } mxq_norm_span;
+typedef enum { MXQ_ROPE_HALVES = 0, MXQ_ROPE_PAIRS = 1 } mxq_rope_style;
+typedef enum { MXQ_KV_BF16 = 0, MXQ_KV_FP8_E4M3 = 1 } mxq_kv_format;
+
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  const float* table;
+  int64_t table_rows;
+  int64_t rot;
+  float eps;
+  mxq_norm_span span;
+  mxq_rope_style style;
+} mxq_norm_rope;
+
+typedef struct {
+  void* k;
+  void* v;
+  int64_t num_pages, page_size, heads, d;
+  int64_t stride_page, stride_token, stride_head; /* elements */
+  mxq_kv_format fmt;
+  float k_scale, v_scale;
+} mxq_paged_kv;
+
+typedef struct {
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* block_table; /* [batch][max_pages] */
+  int64_t batch, max_pages;
+} mxq_paged_batch;
+
+/*
+ * mxq_qk_norm_rope -- q_out = bf16(norm and rotation of Q), k_out likewise, one launch.
+ * q_bf16 [T][ldq] with Hq heads of d, k_bf16 [T][ldk] with Hk heads; either may be NULL (its
+ * other arguments are then ignored).  positions: device int32 [T], or NULL for 0, 1, 2, ...;
+ * a row whose position is outside [0, table_rows) is not written.  Outputs may be the inputs
+ * (same pointer and row stride); otherwise they do not overlap them.  Leading dimensions: at
+ * least heads * d, multiples of 8; 16-byte aligned pointers; heads * d <= 2^16.
+ */
+MXQ_API mxq_status mxq_qk_norm_rope(const mxq_norm_rope* cfg, int64_t T, int64_t d, const void* q_bf16, int64_t Hq,
+                                    int64_t ldq, void* q_out, int64_t ldqo, const void* k_bf16, int64_t Hk,
+                                    int64_t ldk, void* k_out, int64_t ldko, const int32_t* positions,
+                                    mxq_stream_t stream);
+
+/*
+ * mxq_kv_append -- stores the keys (after norm and rotation) and the values of T new rows in
+ * their sequences' pages, and writes q_out = bf16(norm and rotation of Q) when q_bf16 is given,
+ * one launch.  The rotation's position is the token's position in its sequence.  Stored: bf16(y),
+ * or E4M3_RNE_satfinite(fl32(y * fl32(1 / scale))), rounded once from FP32.  Rows of no sequence, and tokens
+ * whose position is negative, beyond the block table or beyond the rotation table, are skipped
+ * (nothing stored, q_out's row not written); a missing page skips the token's key and value only.
+ * Two tokens of one call must not have the same place in the cache.  q_out may be q_bf16.
+ */
+MXQ_API mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* cache, const mxq_paged_batch* batch,
+                                 int64_t T, const void* k_bf16, int64_t ldk, const void* v_bf16, int64_t ldv,
+                                 const void* q_bf16, int64_t Hq, int64_t ldq, void* q_out, int64_t ldqo,
+                                 mxq_stream_t stream);
+
+/*
+ * mxq_attention_paged -- attention of the new tokens of every sequence over its cached keys and
+ * values (the new ones among them), for each query head h with key head h / (Hq / heads):
+ *   O = sum_j softmax_j(scale * q . K_j) V_j
+ * over the keys j < kv_len of pages that are there; with `causal` also j <= the token's position;
+ * with window > 0 (causal only) also j > position - window.  A row that attends nothing is 0;
+ * rows of no sequence are not written.  Lengths are clamped to the block table's capacity.
+ * Softmax statistics and sums are FP32; the weights are rounded to the product's operand type
+ * (BF16; FP16 in the few-row kernel of an E4M3 cache), the result once to BF16.  Cached
+ * positions that no row of a sequence attends may hold anything (NaN, Inf); a non-finite value
+ * of a key attended by some row may reach other rows of the same sequence.
+ *
+ * q_bf16 [T][ldq], out_bf16 [T][ldo] with Hq heads of d, Hq a multiple of the cache's heads, T * Hq <= 2^30;
+ * d 64 or 128 (else MXQ_ERR_UNSUPPORTED).  workspace: device, 256-byte aligned, at least
+ * mxq_attention_paged_workspace_bytes(T, batch, Hq, heads, d) bytes (-1 for invalid arguments);
+ * nothing in it has to be set.  Calls that share a workspace must not overlap.
+ */
+MXQ_API int64_t mxq_attention_paged_workspace_bytes(int64_t T, int64_t batch, int64_t Hq, int64_t heads, int64_t d);
+
+MXQ_API mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_t ldq,
+                                       const mxq_paged_kv* cache, const mxq_paged_batch* batch, int causal,
+                                       int64_t window, float scale, void* workspace, int64_t workspace_bytes,
+                                       void* out_bf16, int64_t ldo, mxq_stream_t stream);
+
+/*
  * mxq_debug_poll -- reads and clears the library's device status word, written by a
  * kernel that gave up one of its bounded waits (each wait on a barrier or a copy is
  * capped at about a second, after which the kernel records MXQ_ERR_TIMEOUT, drains

@@ -16,7 +16,9 @@
 #include "gemm_swap.cuh"
 #include "policy.cuh"
 #include "attention.cuh"
+#include "paged_decode.cuh"
 #include "quantize.cuh"
+#include "rope_cache.cuh"
 
 // Scratch of mxq_linear_w4a4_static: the quantised activations of one call, per device.
 constexpr int64_t kStaticScratchBytes = MXQ_STATIC_SCRATCH_BYTES;
@@ -342,6 +344,148 @@ mxq_status check_quant_args(const void* x, int64_t rows, int64_t K, int64_t ld, 
   if (ld < K || ld % 8 != 0) return MXQ_ERR_ALIGN;
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return MXQ_ERR_ALIGN;
   return MXQ_OK;
+}
+
+// ----------------------------------------------------------------------------- paged cache
+// Norm, rotation and operand checks shared by mxq_qk_norm_rope and mxq_kv_append.
+mxq_status check_norm_rope(const mxq_norm_rope* c, int64_t d) {
+  if (!c) return MXQ_ERR_INVALID_ARG;
+  if (c->span != MXQ_NORM_HEAD && c->span != MXQ_NORM_ROW) return MXQ_ERR_INVALID_ARG;
+  if (c->style != MXQ_ROPE_HALVES && c->style != MXQ_ROPE_PAIRS) return MXQ_ERR_INVALID_ARG;
+  if (!(c->eps >= 0.f) || !std::isfinite(c->eps)) return MXQ_ERR_INVALID_ARG;
+  if ((c->table != nullptr) != (c->rot > 0)) return MXQ_ERR_INVALID_ARG;
+  if (d < 16 || d > 256 || d % 16 != 0 || c->rot < 0 || c->rot > d || c->rot % 16 != 0) return MXQ_ERR_SHAPE;
+  if (c->table && (c->table_rows < 1 || c->table_rows > (int64_t(1) << 31))) return MXQ_ERR_SHAPE;
+  if (!aligned(c->q_weight, 16) || !aligned(c->k_weight, 16) || !aligned(c->table, 16)) return MXQ_ERR_ALIGN;
+  return MXQ_OK;
+}
+
+// A [T][ld] BF16 operand of `heads` heads; null pointers are the caller's to allow.
+mxq_status check_heads(const void* x, int64_t heads, int64_t d, int64_t ld) {
+  if (heads < 1 || heads * d > (int64_t(1) << 16)) return MXQ_ERR_SHAPE;
+  if (ld < heads * d || ld % 8 != 0 || !aligned(x, 16)) return MXQ_ERR_ALIGN;
+  return MXQ_OK;
+}
+
+mxq_status check_paged(const mxq_paged_kv* c, const mxq_paged_batch* b) {
+  if (!c || !b || !c->k || !c->v || !b->cu_q || !b->kv_len || !b->block_table) return MXQ_ERR_INVALID_ARG;
+  if (c->fmt != MXQ_KV_BF16 && c->fmt != MXQ_KV_FP8_E4M3) return MXQ_ERR_INVALID_ARG;
+  const float scales[2] = {c->k_scale, c->v_scale};
+  for (float s : scales)
+    if (!(s > 0.f) || !std::isfinite(s) || !std::isfinite(1.0f / s)) return MXQ_ERR_INVALID_ARG;
+  if (c->fmt == MXQ_KV_BF16 && (c->k_scale != 1.f || c->v_scale != 1.f)) return MXQ_ERR_INVALID_ARG;
+  if (c->num_pages < 1 || c->num_pages > (int64_t(1) << 30)) return MXQ_ERR_SHAPE;
+  if (c->page_size < 8 || c->page_size % 8 != 0 || c->page_size > (int64_t(1) << 20)) return MXQ_ERR_SHAPE;
+  if (c->heads < 1 || c->d < 16 || c->d > 256 || c->d % 16 != 0 || c->heads * c->d > (int64_t(1) << 16))
+    return MXQ_ERR_SHAPE;
+  if (b->batch < 1 || b->batch > (int64_t(1) << 20)) return MXQ_ERR_SHAPE;
+  if (b->max_pages < 1 || b->max_pages > (int64_t(1) << 30) || b->max_pages * c->page_size > (int64_t(1) << 30))
+    return MXQ_ERR_SHAPE;
+  const int64_t size = c->fmt == MXQ_KV_BF16 ? 2 : 1;
+  const int64_t strides[3] = {c->stride_page, c->stride_token, c->stride_head};
+  for (int64_t s : strides)
+    if (s < c->d || s * size % 16 != 0 || s * size >= (int64_t(1) << 40)) return MXQ_ERR_ALIGN;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(b->cu_q, 4) || !aligned(b->kv_len, 4) ||
+      !aligned(b->block_table, 4))
+    return MXQ_ERR_ALIGN;
+  return MXQ_OK;
+}
+
+mxq::RopeParams rope_params(const mxq_norm_rope* c, int64_t T, int64_t d) {
+  mxq::RopeParams p = {};
+  p.table = c->table;
+  p.table_rows = c->table_rows;
+  p.T = T;
+  p.eps = c->eps;
+  p.d = static_cast<int>(d);
+  p.rot = static_cast<int>(c->rot);
+  p.lanes = 1;
+  while (16 * p.lanes < d) p.lanes *= 2;
+  p.pairs = c->style == MXQ_ROPE_PAIRS;
+  p.row_norm = c->span == MXQ_NORM_ROW;
+  return p;
+}
+
+mxq::RopeOperand rope_operand(const void* x, const void* weight, int64_t ld, void* out, int64_t ldo, int64_t heads) {
+  mxq::RopeOperand o = {};
+  if (!x) return o;
+  o.x = static_cast<const uint16_t*>(x);
+  o.weight = static_cast<const uint16_t*>(weight);
+  o.ld = ld;
+  o.out = static_cast<uint16_t*>(out);
+  o.ldo = ldo;
+  o.heads = static_cast<int>(heads);
+  return o;
+}
+
+template <int kCache>
+mxq_status launch_rope_cache(const mxq::RopeParams& p, const mxq::AppendParams& a, cudaStream_t stream) {
+  const int64_t heads = p.q.heads + static_cast<int64_t>(p.k.heads) * (kCache ? 2 : 1);
+  const int64_t want = (heads * p.lanes + 31) / 32 * 32;
+  const int threads = static_cast<int>(std::min<int64_t>(want, mxq::kRopeMaxThreads));
+  return launch_dependent(mxq::rope_cache_kernel<kCache>, dim3(static_cast<unsigned>(p.T)),
+                          dim3(static_cast<unsigned>(threads)), 0, stream, p, a);
+}
+
+// 5-D tensor map over a paged cache: (128-byte piece of a head, token, piece, head, page).
+bool make_tmap_cache(CUtensorMap* m, const mxq_paged_kv* c, const void* base, int box_tokens) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const bool fp8 = c->fmt == MXQ_KV_FP8_E4M3;
+  const uint64_t size = fp8 ? 1 : 2;
+  const uint64_t row = static_cast<uint64_t>(c->d) * size, piece = row > 128 ? 128 : row;
+  const cuuint64_t dims[5] = {piece / size, static_cast<cuuint64_t>(c->page_size), row / piece,
+                              static_cast<cuuint64_t>(c->heads), static_cast<cuuint64_t>(c->num_pages)};
+  const cuuint64_t strides[4] = {c->stride_token * size, piece, c->stride_head * size, c->stride_page * size};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(piece / size), static_cast<cuuint32_t>(box_tokens), 1, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            piece == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace of the paged attention: the parts of units that several CTAs share.
+struct PagedWorkspace {
+  int64_t o = 0, ml = 0, units = 0, bytes = 0;
+};
+
+constexpr int kPagedMaxCtas = 160;  // at least the SMs of any sm_100 device; parts per unit < 4096
+
+PagedWorkspace paged_workspace(int64_t rows, int64_t d) {
+  auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+  PagedWorkspace w;
+  w.ml = up(2 * kPagedMaxCtas * rows * d * 4);
+  w.units = w.ml + up(2 * kPagedMaxCtas * rows * 8);
+  w.bytes = w.units + up(kPagedMaxCtas * 16);
+  return w;
+}
+
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
+template <int D, int kRows>
+mxq_status launch_paged_join(const mxq::PagedParams& p, cudaStream_t stream) {
+  return launch_dependent(mxq::paged_join_kernel<D, kRows>, dim3(static_cast<unsigned>(p.ctas), kRows / 4), dim3(128),
+                          0, stream, p);
+}
+
+template <int D, bool kFp8>
+mxq_status launch_paged_decode(const DeviceInfo& dev, const mxq_paged_kv* c, mxq::PagedParams p,
+                               cudaStream_t stream) {
+  using S = mxq::DecShape<D, kFp8>;
+  auto kernel = mxq::paged_decode_kernel<D, kFp8>;
+  static PerDevice setup;
+  if (!setup.ensure(dev.index, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes) == cudaSuccess;
+      }))
+    return MXQ_ERR_CUDA;
+  p.tile_rows = mxq::kDecRows;
+  p.page_box = gcd(p.page_size, S::kKeys);
+  CUtensorMap tk, tv;
+  if (!make_tmap_cache(&tk, c, c->k, p.page_box) || !make_tmap_cache(&tv, c, c->v, p.page_box)) return MXQ_ERR_CUDA;
+  mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(mxq::kDecThreads), S::kSmemBytes,
+                                   stream, tk, tv, p);
+  return st != MXQ_OK ? st : launch_paged_join<D, mxq::kDecRows>(p, stream);
 }
 
 }  // namespace
@@ -725,6 +869,117 @@ mxq_status mxq_linear_w4a4_static(const void* x_bf16, int64_t M, int64_t K, int6
   // reads (codes of all M rows, whole scale atoms including their padding).
   return mxq_linear_w4a4(x_bf16, M, K, ldx, rule, w_codes, w_sf, N, alpha, bias_bf16, scratch, kStaticScratchBytes,
                          d_bf16, ldd, stream);
+}
+
+mxq_status mxq_qk_norm_rope(const mxq_norm_rope* cfg, int64_t T, int64_t d, const void* q_bf16, int64_t Hq,
+                            int64_t ldq, void* q_out, int64_t ldqo, const void* k_bf16, int64_t Hk, int64_t ldk,
+                            void* k_out, int64_t ldko, const int32_t* positions, mxq_stream_t stream) {
+  mxq_status st = check_norm_rope(cfg, d);
+  if (st != MXQ_OK) return st;
+  if ((!q_bf16 && !k_bf16) || (q_bf16 && !q_out) || (k_bf16 && !k_out)) return MXQ_ERR_INVALID_ARG;
+  if (T < 1 || T > INT32_MAX) return MXQ_ERR_SHAPE;
+  if (q_bf16 && ((st = check_heads(q_bf16, Hq, d, ldq)) != MXQ_OK || (st = check_heads(q_out, Hq, d, ldqo)) != MXQ_OK))
+    return st;
+  if (k_bf16 && ((st = check_heads(k_bf16, Hk, d, ldk)) != MXQ_OK || (st = check_heads(k_out, Hk, d, ldko)) != MXQ_OK))
+    return st;
+  if (!aligned(positions, 4)) return MXQ_ERR_ALIGN;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != MXQ_OK) return st;
+  mxq::RopeParams p = rope_params(cfg, T, d);
+  p.q = rope_operand(q_bf16, cfg->q_weight, ldq, q_out, ldqo, Hq);
+  p.k = rope_operand(k_bf16, cfg->k_weight, ldk, k_out, ldko, Hk);
+  p.positions = positions;
+  return launch_rope_cache<0>(p, mxq::AppendParams{}, stream);
+}
+
+mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* cache, const mxq_paged_batch* batch, int64_t T,
+                         const void* k_bf16, int64_t ldk, const void* v_bf16, int64_t ldv, const void* q_bf16,
+                         int64_t Hq, int64_t ldq, void* q_out, int64_t ldqo, mxq_stream_t stream) {
+  mxq_status st = check_paged(cache, batch);
+  if (st != MXQ_OK) return st;
+  const int64_t d = cache->d;
+  if ((st = check_norm_rope(cfg, d)) != MXQ_OK) return st;
+  if (!k_bf16 || !v_bf16 || (q_bf16 && !q_out)) return MXQ_ERR_INVALID_ARG;
+  if (T < 1 || T > INT32_MAX) return MXQ_ERR_SHAPE;
+  if ((st = check_heads(k_bf16, cache->heads, d, ldk)) != MXQ_OK || (st = check_heads(v_bf16, cache->heads, d, ldv)) != MXQ_OK)
+    return st;
+  if (q_bf16 && ((st = check_heads(q_bf16, Hq, d, ldq)) != MXQ_OK || (st = check_heads(q_out, Hq, d, ldqo)) != MXQ_OK))
+    return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != MXQ_OK) return st;
+  mxq::RopeParams p = rope_params(cfg, T, d);
+  p.q = rope_operand(q_bf16, cfg->q_weight, ldq, q_out, ldqo, Hq);
+  p.k = rope_operand(k_bf16, cfg->k_weight, ldk, nullptr, 0, cache->heads);
+  p.v = static_cast<const uint16_t*>(v_bf16);
+  p.ldv = ldv;
+  mxq::AppendParams a = {};
+  a.cu_q = batch->cu_q;
+  a.kv_len = batch->kv_len;
+  a.block_table = batch->block_table;
+  a.table_stride = batch->max_pages;
+  a.batch = static_cast<int>(batch->batch);
+  a.k_cache = cache->k;
+  a.v_cache = cache->v;
+  a.stride_page = cache->stride_page;
+  a.stride_token = cache->stride_token;
+  a.stride_head = cache->stride_head;
+  a.num_pages = static_cast<int>(cache->num_pages);
+  a.page_size = static_cast<int>(cache->page_size);
+  a.k_inv_scale = 1.0f / cache->k_scale;
+  a.v_inv_scale = 1.0f / cache->v_scale;
+  return cache->fmt == MXQ_KV_BF16 ? launch_rope_cache<1>(p, a, stream) : launch_rope_cache<2>(p, a, stream);
+}
+
+int64_t mxq_attention_paged_workspace_bytes(int64_t T, int64_t batch, int64_t Hq, int64_t Hk, int64_t d) {
+  if (T < 1 || batch < 1 || Hk < 1 || Hq < Hk || Hq % Hk != 0 || (d != 64 && d != 128)) return -1;
+  return paged_workspace(mxq::kDecRows, d).bytes;
+}
+
+mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_t ldq, const mxq_paged_kv* cache,
+                               const mxq_paged_batch* batch, int causal, int64_t window, float scale, void* workspace,
+                               int64_t workspace_bytes, void* out_bf16, int64_t ldo, mxq_stream_t stream) {
+  mxq_status st = check_paged(cache, batch);
+  if (st != MXQ_OK) return st;
+  if (!q_bf16 || !out_bf16 || !workspace) return MXQ_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || window < 0 || (window > 0 && !causal)) return MXQ_ERR_INVALID_ARG;
+  const int64_t d = cache->d, Hk = cache->heads;
+  if (d != 64 && d != 128) return MXQ_ERR_UNSUPPORTED;
+  if (T < 1 || Hq < 1 || Hq % Hk != 0 || T * Hq > (int64_t(1) << 30) || T > (int64_t(1) << 30)) return MXQ_ERR_SHAPE;
+  if (window > (int64_t(1) << 30)) return MXQ_ERR_SHAPE;
+  if ((st = check_heads(q_bf16, Hq, d, ldq)) != MXQ_OK || (st = check_heads(out_bf16, Hq, d, ldo)) != MXQ_OK) return st;
+  if (!aligned(workspace, 256)) return MXQ_ERR_ALIGN;
+  if (workspace_bytes < mxq_attention_paged_workspace_bytes(T, batch->batch, Hq, Hk, d)) return MXQ_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != MXQ_OK) return st;
+
+  const PagedWorkspace ws = paged_workspace(mxq::kDecRows, d);
+  auto* base = static_cast<uint8_t*>(workspace);
+  mxq::PagedParams p = {};
+  p.q = static_cast<const uint16_t*>(q_bf16);
+  p.out = static_cast<uint16_t*>(out_bf16);
+  p.cu_q = batch->cu_q;
+  p.kv_len = batch->kv_len;
+  p.block_table = batch->block_table;
+  p.part_o = reinterpret_cast<float*>(base);
+  p.part_ml = reinterpret_cast<float2*>(base + ws.ml);
+  p.part_units = reinterpret_cast<int4*>(base + ws.units);
+  p.ldq = ldq;
+  p.ldo = ldo;
+  p.T = T;
+  p.table_stride = batch->max_pages;
+  p.batch = static_cast<int>(batch->batch);
+  p.num_pages = static_cast<int>(cache->num_pages);
+  p.page_size = static_cast<int>(cache->page_size);
+  p.Hk = static_cast<int>(Hk);
+  p.G = static_cast<int>(Hq / Hk);
+  p.causal = causal != 0;
+  p.window = static_cast<int>(window);
+  p.ctas = std::min(dev.sm_count, kPagedMaxCtas);
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
+  p.v_scale = cache->v_scale;
+  const bool fp8 = cache->fmt == MXQ_KV_FP8_E4M3;
+  if (d == 128) return fp8 ? launch_paged_decode<128, true>(dev, cache, p, stream) : launch_paged_decode<128, false>(dev, cache, p, stream);
+  return fp8 ? launch_paged_decode<64, true>(dev, cache, p, stream) : launch_paged_decode<64, false>(dev, cache, p, stream);
 }
 
 mxq_status mxq_selftest_wait_timeout(mxq_stream_t stream) {

@@ -24,13 +24,17 @@ STATUS_NAMES = {0: "MXQ_OK", 1: "MXQ_ERR_INVALID_ARG", 2: "MXQ_ERR_SHAPE", 3: "M
                 4: "MXQ_ERR_UNSUPPORTED", 5: "MXQ_ERR_CUDA", 6: "MXQ_ERR_TIMEOUT"}
 MXQ_SCALE_OCP, MXQ_SCALE_UOS = 0, 1
 MXQ_ACT_MXFP4, MXQ_ACT_FP8_E4M3 = 0, 1
+MXQ_NORM_HEAD, MXQ_NORM_ROW = 0, 1
+MXQ_ROPE_HALVES, MXQ_ROPE_PAIRS = 0, 1
+MXQ_KV_BF16, MXQ_KV_FP8_E4M3 = 0, 1
 MXQ_PREC_W4A4, MXQ_PREC_W4A4_TRANSFORM, MXQ_PREC_W4A8, MXQ_PREC_BF16 = 0, 1, 2, 3
 
 EXPORTED = ("mxq_status_string", "mxq_sf_bytes", "mxq_quantize_act", "mxq_pack_weight", "mxq_gemm_w4a4",
             "mxq_gemm_w4a8", "mxq_dequant_mxfp4", "mxq_qdq_act", "mxq_channel_absmax", "mxq_smooth_factors",
             "mxq_quantize_smooth", "mxq_sqnr_accumulate", "mxq_sqnr_db", "mxq_select_precision", "mxq_attn_padded_keys",
             "mxq_attn_code_poly", "mxq_quantize_vt",
-            "mxq_attention_mxfp4", "mxq_linear_workspace_bytes", "mxq_linear_w4a4", "mxq_linear_w4a4_static",
+            "mxq_attention_mxfp4", "mxq_qk_norm_rope", "mxq_kv_append", "mxq_attention_paged_workspace_bytes",
+            "mxq_attention_paged", "mxq_linear_workspace_bytes", "mxq_linear_w4a4", "mxq_linear_w4a4_static",
             "mxq_debug_poll", "mxq_selftest_wait_timeout")
 
 
@@ -38,6 +42,27 @@ class MxqError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}")
         self.status = status
+
+
+class NormRope(ctypes.Structure):
+    """mxq_norm_rope: norm weights and epsilon, rotation table and style."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("table_rows", ctypes.c_int64), ("rot", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("span", ctypes.c_int), ("style", ctypes.c_int)]
+
+
+class PagedKVArgs(ctypes.Structure):
+    """mxq_paged_kv: buffers, sizes, strides (elements) and format of a paged cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("heads", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("stride_page", ctypes.c_int64), ("stride_token", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("fmt", ctypes.c_int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class PagedBatchArgs(ctypes.Structure):
+    """mxq_paged_batch: row offsets, lengths and pages of a batch of sequences."""
+    _fields_ = [("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("batch", ctypes.c_int64), ("max_pages", ctypes.c_int64)]
 
 
 _lib = None
@@ -88,6 +113,14 @@ def lib() -> ctypes.CDLL:
     L.mxq_attn_code_poly.restype = None
     L.mxq_attention_mxfp4.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, I32, P, I64, P]
     L.mxq_attention_mxfp4.restype = I32
+    L.mxq_qk_norm_rope.argtypes = [P, I64, I64, P, I64, I64, P, I64, P, I64, I64, P, I64, P, P]
+    L.mxq_qk_norm_rope.restype = I32
+    L.mxq_kv_append.argtypes = [P, P, P, I64, P, I64, P, I64, P, I64, I64, P, I64, P]
+    L.mxq_kv_append.restype = I32
+    L.mxq_attention_paged_workspace_bytes.argtypes = [I64] * 5
+    L.mxq_attention_paged_workspace_bytes.restype = I64
+    L.mxq_attention_paged.argtypes = [P, I64, I64, I64, P, P, I32, I64, F32, P, I64, P, I64, P]
+    L.mxq_attention_paged.restype = I32
     L.mxq_linear_workspace_bytes.argtypes = [I64, I64]
     L.mxq_linear_workspace_bytes.restype = I64
     L.mxq_linear_w4a4.argtypes = [P, I64, I64, I64, I32, P, P, I64, F32, P, P, I64, P, I64, P]
@@ -217,6 +250,29 @@ def mxq_attention_mxfp4(q_codes, q_sf, k_codes, k_sf, vt_codes, vt_sf, S_q, S_kv
     _check(lib().mxq_attention_mxfp4(_ptr(q_codes), _ptr(q_sf), _ptr(k_codes), _ptr(k_sf), _ptr(vt_codes),
                                      _ptr(vt_sf), int(S_q), int(S_kv), int(H), int(d), int(rule), _ptr(out),
                                      int(ldo), _stream(stream)), "mxq_attention_mxfp4")
+
+
+def mxq_qk_norm_rope(cfg: NormRope, T, d, q, Hq, ldq, q_out, ldqo, k, Hk, ldk, k_out, ldko, positions,
+                     stream=None) -> None:
+    _check(lib().mxq_qk_norm_rope(ctypes.byref(cfg), T, d, _ptr(q), Hq, ldq, _ptr(q_out), ldqo, _ptr(k), Hk, ldk,
+                                  _ptr(k_out), ldko, _ptr(positions), _stream(stream)), "mxq_qk_norm_rope")
+
+
+def mxq_kv_append(cfg: NormRope, cache: PagedKVArgs, batch: PagedBatchArgs, T, k, ldk, v, ldv, q, Hq, ldq, q_out, ldqo,
+                  stream=None) -> None:
+    _check(lib().mxq_kv_append(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(batch), T, _ptr(k), ldk, _ptr(v),
+                               ldv, _ptr(q), Hq, ldq, _ptr(q_out), ldqo, _stream(stream)), "mxq_kv_append")
+
+
+def mxq_attention_paged_workspace_bytes(T: int, batch: int, Hq: int, heads: int, d: int) -> int:
+    return int(lib().mxq_attention_paged_workspace_bytes(T, batch, Hq, heads, d))
+
+
+def mxq_attention_paged(q, T, Hq, ldq, cache: PagedKVArgs, batch: PagedBatchArgs, causal, window, scale, workspace,
+                        workspace_bytes, out, ldo, stream=None) -> None:
+    _check(lib().mxq_attention_paged(_ptr(q), T, Hq, ldq, ctypes.byref(cache), ctypes.byref(batch), int(bool(causal)),
+                                     window, scale, _ptr(workspace), workspace_bytes, _ptr(out), ldo, _stream(stream)),
+           "mxq_attention_paged")
 
 
 def mxq_linear_workspace_bytes(M: int, K: int) -> int:
@@ -473,3 +529,180 @@ def linear_w4a8(x: torch.Tensor, act_scale: float, w_codes, w_sf, N: int, bias=N
     M, K = x.shape
     q = quantize_act_fp8(x, act_scale, stream=stream)
     return gemm_w4a8(q, act_scale, w_codes, w_sf, M, N, K, bias, stream=stream)
+
+
+# ------------------------------------------------------------------ queries and keys, paged cache
+def _heads_2d(x: torch.Tensor, heads: int, d: int | None, name: str) -> int:
+    """Checks a [T][heads * d] operand and returns d."""
+    _bf16_2d(x, name)
+    width = x.shape[1]
+    if heads < 1 or width % heads or (d is not None and width != heads * d):
+        raise ValueError(f"{name}: {width} columns are not {heads} heads" + ("" if d is None else f" of {d}"))
+    return width // heads
+
+
+def _int32(x: torch.Tensor, shape: tuple, name: str) -> int:
+    if x.dtype != torch.int32 or not x.is_cuda or not x.is_contiguous() or tuple(x.shape) != shape:
+        raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor of shape {shape}")
+    _on_current_device(x, name)
+    return x.data_ptr()
+
+
+def _norm_rope(q_heads, k_heads, d, q_weight, k_weight, eps, span, table, style) -> NormRope:
+    cfg = NormRope(None, None, None, 0, 0, eps, span, style)
+    for name, w, heads in (("q_weight", q_weight, q_heads), ("k_weight", k_weight, k_heads)):
+        if w is None:
+            continue
+        n = heads * d if span == MXQ_NORM_ROW else d
+        if w.dtype != torch.bfloat16 or not w.is_cuda or not w.is_contiguous() or w.numel() != n:
+            raise ValueError(f"{name}: expected {n} contiguous bfloat16 values on the GPU")
+        _on_current_device(w, name)
+        setattr(cfg, name, w.data_ptr())
+    if table is not None:
+        if table.dtype != torch.float32 or not table.is_cuda or table.dim() != 2 or not table.is_contiguous():
+            raise ValueError("table: expected a contiguous float32 CUDA tensor [positions][rot]")
+        _on_current_device(table, "table")
+        cfg.table, cfg.table_rows, cfg.rot = table.data_ptr(), table.shape[0], table.shape[1]
+    return cfg
+
+
+def rope_table(positions: int | torch.Tensor, rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """FP32 [positions][rot]: cos, then sin, of position * base^(-2 i / rot), the angles in 64 bits.
+    `positions`: how many (0, 1, 2, ...), or a 1-D tensor of positions (one row of the table each)."""
+    pos = torch.arange(positions, device=device) if isinstance(positions, int) else positions.to(device)
+    inv = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    angle = pos.to(torch.float64)[:, None] * inv
+    return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32)
+
+
+class PagedKV:
+    """A paged key / value cache: k and v [pages][page_size][heads][d], BF16 or E4M3 (float8_e4m3fn or
+    uint8), with contiguous heads; other orders of the dimensions are views with other strides.
+    k_scale, v_scale: static scales of an E4M3 cache."""
+
+    __slots__ = ("k", "v", "args")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
+        shape, strides = k.shape, k.stride()
+        if len(shape) != 4 or v.shape != shape or v.stride() != strides or v.dtype != k.dtype:
+            raise ValueError("k, v: expected two [pages][page_size][heads][d] tensors alike in shape, strides and type")
+        if k.dtype == torch.bfloat16:
+            fmt = MXQ_KV_BF16
+        elif k.dtype in (torch.float8_e4m3fn, torch.uint8):
+            fmt = MXQ_KV_FP8_E4M3
+        else:
+            raise ValueError("k, v: expected bfloat16, float8_e4m3fn or uint8")
+        if not k.is_cuda or not v.is_cuda or strides[3] != 1:
+            raise ValueError("k, v: expected CUDA tensors with contiguous heads")
+        _on_current_device(k, "k")
+        _on_current_device(v, "v")
+        self.k, self.v = k, v
+        self.args = PagedKVArgs(k.data_ptr(), v.data_ptr(), *shape, *strides[:3], fmt, k_scale, v_scale)
+
+
+def paged_kv(pages: int, page_size: int, heads: int, d: int, fmt: int = MXQ_KV_BF16, k_scale: float = 1.0,
+             v_scale: float = 1.0, device="cuda") -> PagedKV:
+    """Allocates a cache (its contents are undefined until tokens are appended)."""
+    dtype = torch.bfloat16 if fmt == MXQ_KV_BF16 else torch.float8_e4m3fn
+    k, v = (torch.empty(pages, page_size, heads, d, dtype=dtype, device=device) for _ in range(2))
+    return PagedKV(k, v, k_scale, v_scale)
+
+
+class PagedBatch:
+    """The sequences of a call: cu_q [batch + 1], kv_len [batch] and block_table [batch][max_pages], int32 on
+    the GPU (see mxq_paged_batch).  Holds the tensors: their contents may change between calls."""
+
+    __slots__ = ("cu_q", "kv_len", "block_table", "args")
+
+    def __init__(self, cu_q: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor):
+        if block_table.dim() != 2:
+            raise ValueError("block_table: expected [batch][max_pages]")
+        batch, max_pages = block_table.shape
+        self.cu_q, self.kv_len, self.block_table = cu_q, kv_len, block_table
+        self.args = PagedBatchArgs(_int32(cu_q, (batch + 1,), "cu_q"), _int32(kv_len, (batch,), "kv_len"),
+                                   _int32(block_table, (batch, max_pages), "block_table"), batch, max_pages)
+
+
+def _out_heads(out, x: torch.Tensor, name: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    _bf16_2d(out, name)
+    if out.shape != x.shape:
+        raise ValueError(f"{name}: expected shape {tuple(x.shape)}")
+    return out
+
+
+@_on_stream
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, Hq: int, Hk: int, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 span: int = MXQ_NORM_HEAD, table=None, positions=None, style: int = MXQ_ROPE_HALVES, q_out=None,
+                 k_out=None, stream=None):
+    """Norm (where weights are given) and rotation (where a table is given) of q [T][Hq*d] and k
+    [T][Hk*d] -> (q_out, k_out).  positions: int32 [T], or None for 0, 1, 2, ...; a row whose position is
+    outside the table is not written.  q_out=q, k_out=k work in place."""
+    d = _heads_2d(q, Hq, None, "q")
+    _heads_2d(k, Hk, d, "k")
+    T = q.shape[0]
+    if k.shape[0] != T:
+        raise ValueError("q, k: expected the same number of rows")
+    cfg = _norm_rope(Hq, Hk, d, q_weight, k_weight, eps, span, table, style)
+    pos = None if positions is None else _int32(positions, (T,), "positions")
+    qo, ko = _out_heads(q_out, q, "q_out"), _out_heads(k_out, k, "k_out")
+    mxq_qk_norm_rope(cfg, T, d, q.data_ptr(), Hq, q.stride(0), qo.data_ptr(), qo.stride(0), k.data_ptr(), Hk,
+                     k.stride(0), ko.data_ptr(), ko.stride(0), pos, stream)
+    return qo, ko
+
+
+@_on_stream
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKV, batch: PagedBatch, k_weight=None, eps: float = 1e-6,
+              span: int = MXQ_NORM_HEAD, table=None, style: int = MXQ_ROPE_HALVES, q=None, q_weight=None, q_out=None,
+              stream=None):
+    """Norm and rotation of the new keys k [T][heads*d] at their sequences' positions, keys and values
+    into the cache; with q [T][Hq*d] also its norm and rotation -> q_out (else None)."""
+    a = cache.args
+    d, heads = a.d, a.heads
+    _heads_2d(k, heads, d, "k")
+    _heads_2d(v, heads, d, "v")
+    _on_current_device(cache.k, "cache")
+    _on_current_device(batch.cu_q, "batch")
+    T = k.shape[0]
+    if v.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("k, v, q: expected the same number of rows")
+    if q is None:
+        cfg = _norm_rope(0, heads, d, None, k_weight, eps, span, table, style)
+        mxq_kv_append(cfg, a, batch.args, T, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), None, 0, 0, None, 0,
+                      stream)
+        return None
+    _bf16_2d(q, "q")
+    Hq = q.shape[1] // d
+    _heads_2d(q, Hq, d, "q")
+    cfg = _norm_rope(Hq, heads, d, q_weight, k_weight, eps, span, table, style)
+    qo = _out_heads(q_out, q, "q_out")
+    mxq_kv_append(cfg, a, batch.args, T, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), q.data_ptr(), Hq,
+                  q.stride(0), qo.data_ptr(), qo.stride(0), stream)
+    return qo
+
+
+def attention_paged_workspace(T: int, batch: int, Hq: int, heads: int, d: int, device) -> torch.Tensor:
+    """A workspace for attention_paged."""
+    n = mxq_attention_paged_workspace_bytes(T, batch, Hq, heads, d)
+    if n < 0:
+        raise ValueError("attention_paged_workspace: invalid sizes (d 64 or 128, Hq a multiple of heads)")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+@_on_stream
+def attention_paged(q: torch.Tensor, Hq: int, cache: PagedKV, batch: PagedBatch, causal: bool = True, window: int = 0,
+                    scale: float | None = None, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of the new tokens' queries q [T][Hq*d] over their sequences' cached keys and values
+    -> O [T][Hq*d] BF16.  scale: d^-1/2 by default.  Rows of no sequence are not written."""
+    a, b = cache.args, batch.args
+    d = _heads_2d(q, Hq, a.d, "q")
+    _on_current_device(cache.k, "cache")
+    _on_current_device(batch.cu_q, "batch")
+    T = q.shape[0]
+    if workspace is None:
+        workspace = attention_paged_workspace(T, b.batch, Hq, a.heads, d, q.device)
+    o = _out_heads(out, q, "out")
+    mxq_attention_paged(q.data_ptr(), T, Hq, q.stride(0), a, b, causal, window, d ** -0.5 if scale is None else scale,
+                        workspace, workspace.numel() * workspace.element_size(), o.data_ptr(), o.stride(0), stream)
+    return o
