@@ -467,7 +467,7 @@ MXQ_API mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* c
 /*
  * mxq_attention_paged -- attention of the new tokens of every sequence over its cached keys and
  * values (the new ones among them), for each query head h with key head h / (Hq / heads):
- *   O = sum_j softmax_j(scale * q . K_j) V_j
+ *   O = sum_j softmax_j(scale * q . K_j) V_j,  scale >= 0,
  * over the keys j < kv_len of pages that are there; with `causal` also j <= the token's position;
  * with window > 0 (causal only) also j > position - window.  A row that attends nothing is 0;
  * rows of no sequence are not written.  Lengths are clamped to the block table's capacity.

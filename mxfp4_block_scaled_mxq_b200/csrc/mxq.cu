@@ -16,6 +16,7 @@
 #include "gemm_swap.cuh"
 #include "policy.cuh"
 #include "attention.cuh"
+#include "paged_chunk.cuh"
 #include "paged_decode.cuh"
 #include "quantize.cuh"
 #include "rope_cache.cuh"
@@ -461,6 +462,11 @@ PagedWorkspace paged_workspace(int64_t rows, int64_t d) {
   return w;
 }
 
+// Which kernel: the few-row one streams the cache once per 16 rows, the other computes 128 rows of
+// a tile whether they are there or not.  By the mean, since the lengths are on the device:
+// either kernel is right for any.
+bool paged_many_rows(int64_t T, int64_t batch, int64_t G) { return G <= mxq::kChunkHalf && T * G > 32 * batch; }
+
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 template <int D, int kRows>
@@ -486,6 +492,44 @@ mxq_status launch_paged_decode(const DeviceInfo& dev, const mxq_paged_kv* c, mxq
   mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(mxq::kDecThreads), S::kSmemBytes,
                                    stream, tk, tv, p);
   return st != MXQ_OK ? st : launch_paged_join<D, mxq::kDecRows>(p, stream);
+}
+
+// Q as (128-byte piece, piece, head, token): a box is one piece of the G heads of whole tokens.
+bool make_tmap_q(CUtensorMap* m, const mxq::PagedParams& p, int64_t d, int tokens) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(p.Hk) * p.G,
+                              static_cast<cuuint64_t>(p.T)};
+  const cuuint64_t strides[3] = {128, static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(p.ldq) * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(p.q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool kFp8>
+mxq_status launch_paged_chunk(const DeviceInfo& dev, const mxq_paged_kv* c, mxq::PagedParams p, cudaStream_t stream) {
+  using S = mxq::ChunkShape<D, kFp8>;
+  auto kernel = mxq::paged_chunk_kernel<D, kFp8>;
+  static PerDevice setup;
+  if (!setup.ensure(dev.index, [&] {
+        // the register split must be covered by what the kernel is launched with: setmaxnreg waits otherwise
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, kernel) == cudaSuccess && a.numRegs == S::kLaunchRegs &&
+               cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes) == cudaSuccess;
+      }))
+    return MXQ_ERR_CUDA;
+  const int tokens = mxq::kChunkHalf / p.G;  // whole tokens of a half
+  p.tile_rows = 2 * tokens * p.G;
+  p.page_box = gcd(p.page_size, mxq::kChunkKeys);
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap_q(&tq, p, D, tokens) || !make_tmap_cache(&tk, c, c->k, p.page_box) ||
+      !make_tmap_cache(&tv, c, c->v, p.page_box))
+    return MXQ_ERR_CUDA;
+  mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(S::kThreads), S::kSmemBytes,
+                                   stream, tq, tk, tv, p);
+  return st != MXQ_OK ? st : launch_paged_join<D, mxq::kChunkRows>(p, stream);
 }
 
 }  // namespace
@@ -932,7 +976,7 @@ mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* cache, co
 
 int64_t mxq_attention_paged_workspace_bytes(int64_t T, int64_t batch, int64_t Hq, int64_t Hk, int64_t d) {
   if (T < 1 || batch < 1 || Hk < 1 || Hq < Hk || Hq % Hk != 0 || (d != 64 && d != 128)) return -1;
-  return paged_workspace(mxq::kDecRows, d).bytes;
+  return paged_workspace(paged_many_rows(T, batch, Hq / Hk) ? mxq::kChunkRows : mxq::kDecRows, d).bytes;
 }
 
 mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_t ldq, const mxq_paged_kv* cache,
@@ -941,7 +985,7 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
   mxq_status st = check_paged(cache, batch);
   if (st != MXQ_OK) return st;
   if (!q_bf16 || !out_bf16 || !workspace) return MXQ_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || window < 0 || (window > 0 && !causal)) return MXQ_ERR_INVALID_ARG;
+  if (!(scale >= 0.f) || !std::isfinite(scale) || window < 0 || (window > 0 && !causal)) return MXQ_ERR_INVALID_ARG;
   const int64_t d = cache->d, Hk = cache->heads;
   if (d != 64 && d != 128) return MXQ_ERR_UNSUPPORTED;
   if (T < 1 || Hq < 1 || Hq % Hk != 0 || T * Hq > (int64_t(1) << 30) || T > (int64_t(1) << 30)) return MXQ_ERR_SHAPE;
@@ -952,7 +996,8 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
   DeviceInfo dev;
   if ((st = current_device(&dev)) != MXQ_OK) return st;
 
-  const PagedWorkspace ws = paged_workspace(mxq::kDecRows, d);
+  const bool many = paged_many_rows(T, batch->batch, Hq / Hk);
+  const PagedWorkspace ws = paged_workspace(many ? mxq::kChunkRows : mxq::kDecRows, d);
   auto* base = static_cast<uint8_t*>(workspace);
   mxq::PagedParams p = {};
   p.q = static_cast<const uint16_t*>(q_bf16);
@@ -978,8 +1023,18 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
   p.v_scale = cache->v_scale;
   const bool fp8 = cache->fmt == MXQ_KV_FP8_E4M3;
-  if (d == 128) return fp8 ? launch_paged_decode<128, true>(dev, cache, p, stream) : launch_paged_decode<128, false>(dev, cache, p, stream);
-  return fp8 ? launch_paged_decode<64, true>(dev, cache, p, stream) : launch_paged_decode<64, false>(dev, cache, p, stream);
+  if (many) {
+    if (d == 128)
+      return fp8 ? launch_paged_chunk<128, true>(dev, cache, p, stream)
+                 : launch_paged_chunk<128, false>(dev, cache, p, stream);
+    return fp8 ? launch_paged_chunk<64, true>(dev, cache, p, stream)
+               : launch_paged_chunk<64, false>(dev, cache, p, stream);
+  }
+  if (d == 128)
+    return fp8 ? launch_paged_decode<128, true>(dev, cache, p, stream)
+               : launch_paged_decode<128, false>(dev, cache, p, stream);
+  return fp8 ? launch_paged_decode<64, true>(dev, cache, p, stream)
+             : launch_paged_decode<64, false>(dev, cache, p, stream);
 }
 
 mxq_status mxq_selftest_wait_timeout(mxq_stream_t stream) {
