@@ -471,7 +471,7 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
 template <int D, int kRows>
 mxq_status launch_paged_join(const mxq::PagedParams& p, cudaStream_t stream) {
-  return launch_dependent(mxq::paged_join_kernel<D, kRows>, dim3(static_cast<unsigned>(p.ctas), kRows / 4), dim3(128),
+  return launch_dependent(mxq::paged_join_kernel<D, kRows>, dim3(static_cast<unsigned>(p.ctas), kRows / 8), dim3(128),
                           0, stream, p);
 }
 
@@ -522,7 +522,7 @@ mxq_status launch_paged_chunk(const DeviceInfo& dev, const mxq_paged_kv* c, mxq:
     return MXQ_ERR_CUDA;
   const int tokens = mxq::kChunkHalf / p.G;  // whole tokens of a half
   p.tile_rows = 2 * tokens * p.G;
-  p.page_box = gcd(p.page_size, mxq::kChunkKeys);
+  p.page_box = gcd(p.page_size, kFp8 ? S::kRawKeys : mxq::kChunkKeys);
   CUtensorMap tq, tk, tv;
   if (!make_tmap_q(&tq, p, D, tokens) || !make_tmap_cache(&tk, c, c->k, p.page_box) ||
       !make_tmap_cache(&tv, c, c->v, p.page_box))
@@ -1017,6 +1017,7 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
   p.page_size = static_cast<int>(cache->page_size);
   p.Hk = static_cast<int>(Hk);
   p.G = static_cast<int>(Hq / Hk);
+  p.out32 = ldo % 16 == 0 && aligned(out_bf16, 32);  // and d % 16 == 0
   p.causal = causal != 0;
   p.window = static_cast<int>(window);
   p.ctas = std::min(dev.sm_count, kPagedMaxCtas);

@@ -26,7 +26,7 @@ struct PagedParams {
   const int32_t* cu_q;
   const int32_t* kv_len;
   const int32_t* block_table;
-  float* part_o;     // [2 ctas][rows][d]
+  float* part_o;     // [2 ctas][d / 4][rows][4]
   float2* part_ml;   // [2 ctas][rows]: (row maximum, row sum)
   int4* part_units;  // [ctas]: the unit that CTA c begins and does not finish: (the sequence's first
                      // row of Q, row tile, rows in it, key head * 4096 + parts); parts 0: none
@@ -35,6 +35,7 @@ struct PagedParams {
   int Hk, G;
   int tile_rows;       // rows (token, head of the group) in a row tile
   int causal, window;  // window 0: none
+  int out32;           // rows of `out` are 32-byte aligned
   int page_box;        // keys per TMA box: gcd(page size, key tile)
   int ctas;            // that share the work (the partial slots' count is twice that)
   float scale_log2;    // scale * log2(e) * k_scale
@@ -133,7 +134,7 @@ struct Share {
 };
 
 struct ShareScratch {
-  int64_t warp_sum[16];
+  int64_t warp_sum[32];
   int64_t weight, rest;
   int b;
 };
@@ -144,7 +145,7 @@ struct ShareScratch {
 template <int kKeys, int kThreads, int kMinTiles>
 __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& sc) {
   constexpr int kWarps = kThreads / 32;
-  static_assert(kWarps <= 16, "scratch");
+  static_assert(kWarps <= 32, "scratch");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool by_warp = p.batch <= kWarps;
   const int per_round = by_warp ? kWarps : kThreads;
@@ -254,42 +255,44 @@ __device__ __forceinline__ int64_t row_offset(const PagedParams& p, int64_t q0, 
 }
 
 // Joins the parts of the unit that CTA blockIdx.x began: its last slot, then the first slots
-// of the CTAs after it.  A warp per row; each lane holds D / 32 columns.
+// of the CTAs after it.  A block has 8 rows x 16 groups of D / 16 columns: the parts' loads are
+// consecutive over the rows, the result's over the columns.
 template <int D, int kRows>
 __global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p) {
-  constexpr int kCols = D / 32;
+  constexpr int kGroup = D / 16;   // columns of a thread
+  constexpr int kVec = kGroup / 4;
   griddep_wait();
   const int c = blockIdx.x;
   const int4 un = p.part_units[c];
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int parts = un.w & 4095;
+  const int r = blockIdx.y * 8 + (threadIdx.x & 7), group = threadIdx.x >> 3;
   if (parts == 0 || r >= un.z) return;
-  const int lane = threadIdx.x & 31;
-  auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * kRows + r; };
+  auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)); };
   float m = -INFINITY;
-  for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[slot(i)].x);
-  for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  for (int i = 0; i < parts; ++i) m = fmaxf(m, p.part_ml[slot(i) * kRows + r].x);
   const float base = m == -INFINITY ? 0.f : m;
-  float acc[kCols] = {}, l = 0.f;
+  float acc[kGroup] = {}, l = 0.f;
 #pragma unroll 4
   for (int i = 0; i < parts; ++i) {
-    const float2 ml = p.part_ml[slot(i)];
+    const float2 ml = p.part_ml[slot(i) * kRows + r];
     const float f = exp2f(ml.x - base);
     l = fmaf(ml.y, f, l);
-    const float* o = p.part_o + slot(i) * D + lane * kCols;
-    float v[kCols];
-    if constexpr (kCols == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
-    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+    const float4* o = reinterpret_cast<const float4*>(p.part_o) + (slot(i) * (D / 4) + group * kVec) * kRows + r;
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) acc[k] = fmaf(v[k], f, acc[k]);
+    for (int k = 0; k < kVec; ++k) {
+      const float4 v = o[k * kRows];
+      acc[4 * k] = fmaf(v.x, f, acc[4 * k]);
+      acc[4 * k + 1] = fmaf(v.y, f, acc[4 * k + 1]);
+      acc[4 * k + 2] = fmaf(v.z, f, acc[4 * k + 2]);
+      acc[4 * k + 3] = fmaf(v.w, f, acc[4 * k + 3]);
+    }
   }
   const float inv = l == 0.f ? 0.f : p.v_scale / l;
-  uint32_t w[kCols / 2];
+  uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + group * kGroup;
 #pragma unroll
-  for (int k = 0; k < kCols / 2; ++k) w[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-  uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + lane * kCols;
-  if constexpr (kCols == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+  for (int k = 0; k < kVec; ++k)
+    *reinterpret_cast<uint2*>(dst + 4 * k) = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
+                                                        pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
 }
 
 }  // namespace mxq

@@ -500,11 +500,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
               make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
                          pack_bf16x2(acc[6], acc[7]));
         } else {
-          const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (tile == 0 ? 1 : 0)) * kDecRows + row;
-          float* dst = p.part_o + slot * D + col;
-          *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          *reinterpret_cast<float4*>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
-          if (col == 0) p.part_ml[slot] = make_float2(top, sum);
+          const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (tile == 0 ? 1 : 0);
+          float4* dst = reinterpret_cast<float4*>(p.part_o) + (slot * (D / 4) + col / 4) * kDecRows + row;
+          dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          dst[kDecRows] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+          if (col == 0) p.part_ml[slot * kDecRows + row] = make_float2(top, sum);
         }
       }
     }
