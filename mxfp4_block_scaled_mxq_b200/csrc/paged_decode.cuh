@@ -1,9 +1,10 @@
 // paged_decode.cuh -- attention of few rows (generated or drafted tokens) over a paged cache.
 //
 // The cache is read once and little is computed on it, so this kernel is bound by DRAM.  One
-// CTA per SM: a producer warp keeps a ring of key tiles (K and V of kKeys keys, TMA boxes of one
+// CTA per SM: producer warps keep a ring of key tiles (K and V of kKeys keys, TMA boxes of one
 // page each, zero fill for pages that are missing) full in shared memory, up to 180 KB in
-// flight, across units; eight consumer warps take the tiles in turn.  A warp holds 16 rows
+// flight, across units; eight consumer warps take the tiles in turn.  Four producer warps, since
+// one needs about 1000 cycles for a tile's pages and copies and 16 KB a tile have to come every 700.  A warp holds 16 rows
 // and its own running maximum, sum and accumulator, so nothing is exchanged per tile: scores
 // by mma.sync m16n8k16 (the rows are too few for a tcgen05 tile of 128), one online-softmax
 // step in base 2, then P V with P in registers.  At the end of a unit the eight warps' states
@@ -25,7 +26,8 @@ namespace mxq {
 
 constexpr int kDecRows = 16;
 constexpr int kDecWarps = 8;
-constexpr int kDecThreads = 32 * (kDecWarps + 1);
+constexpr int kDecProducers = 4;
+constexpr int kDecThreads = 32 * (kDecWarps + kDecProducers);
 constexpr int kDecMaxStages = 24;
 constexpr int kDecMinTiles = 4;
 
@@ -41,7 +43,12 @@ struct DecShape {
   static constexpr int kMlBytes = 2 * kDecWarps * kDecRows * 8;
   static constexpr int kFixed = 1024 + kMergeBytes + kMlBytes + kDecMaxStages * 20 + 512;
   static constexpr int kFit = (225 * 1024 - kFixed) / kStageBytes;
-  static constexpr int kStages = kFit < kDecMaxStages ? kFit : kDecMaxStages;
+  // A stage is always filled by the same producer warp and read by the same consumer warp, each in
+  // order: a warp that met the stage of another could be two rounds from it, where a barrier's
+  // parity says nothing.
+  static constexpr int kStages = (kFit < kDecMaxStages ? kFit : kDecMaxStages) / kDecWarps * kDecWarps;
+  static constexpr int kOwnStages = kStages / kDecProducers;
+  static_assert(kStages >= kDecWarps && kDecWarps % kDecProducers == 0, "stages");
   static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
 };
 
@@ -143,41 +150,39 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   __syncthreads();
   if (sh.count == 0) return;
 
-  if (warp == kDecWarps) {
-    // ------------------------------------------------------------------ producer
+  if (warp >= kDecWarps) {
+    // ------------------------------------------------------------------ producers
     Unit u = sh.u;
     int tile = sh.tile;
     const int nbox = kKeys / p.page_box;
-    int stage = 0;
+    int own = 0;                  // this warp's next stage among its own
+    int turn = warp - kDecWarps;  // tiles until its next one
     uint32_t phase = 0;
     bool ok = true;
     int64_t left = sh.count;
     uint32_t issued = 0, issued_phase = 0;
-    int64_t batch_at = -1;  // block-table entries [batch_at, +32) of sequence batch_b in the lanes
-    int batch_b = -1, entries = -1;
-    while (left > 0) {
+    int batch_at = -1, batch_b = -1, entries = -1;  // block-table entries [batch_at, +32) of sequence batch_b
+    while (ok && left > 0) {
       const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
-      const int64_t row = static_cast<int64_t>(u.b) * p.table_stride;
-      for (int k = 0; k < n; ++k) {
+      const int32_t* table = p.block_table + static_cast<int64_t>(u.b) * p.table_stride;
+      int k = turn;
+      for (; k < n; k += kDecProducers) {
+        const int stage = (warp - kDecWarps) * S::kOwnStages + own;
         const int key0 = (u.kt0 + tile + k) * kKeys;
         // pages of the tile's boxes: lane i < nbox has box i
         const int box_key = key0 + lane * p.page_box;
-        const int64_t entry = box_key / p.page_size;
-        const int64_t first = key0 / p.page_size;
-        if (batch_b != u.b || batch_at < 0 || first < batch_at || first + nbox > batch_at + 32) {
+        const int first = key0 / p.page_size, entry = box_key / p.page_size;
+        if (batch_b != u.b || first < batch_at || first + nbox > batch_at + 32) {
           batch_b = u.b;
           batch_at = first;
-          const int64_t e = first + lane;
-          entries = e < p.table_stride ? p.block_table[row + e] : -1;
+          entries = first + lane < p.table_stride ? table[first + lane] : -1;
         }
-        int page = __shfl_sync(0xffffffffu, entries, static_cast<int>(min(entry - batch_at, int64_t(31))));
+        const int page = __shfl_sync(0xffffffffu, entries, min(entry - batch_at, 31));
         const bool need = lane < nbox && box_key < u.hi && box_key + p.page_box > u.lo;
         const bool there = need && page >= 0 && page < p.num_pages;
         const uint32_t mask = __ballot_sync(0xffffffffu, there);
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1))) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1));
+        if (!ok) break;
         issued |= 1u << stage;
         issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
         if (lane == 0) {
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         __syncwarp();
         if (lane < nbox) {
           const int pg = there ? page : -1;  // out of range: the box is filled with zeros
-          const int in_page = there ? box_key - static_cast<int>(entry) * p.page_size : 0;
+          const int in_page = there ? box_key - entry * p.page_size : 0;
           uint8_t* dst = ring + stage * S::kStageBytes + lane * p.page_box * S::kBoxRowBytes;
 #pragma unroll
           for (int h = 0; h < S::kHalves; ++h) {
@@ -195,12 +200,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             tma_load_5d(dst + S::kTileBytes + h * kKeys * 128, &tmap_v, 0, in_page, h, u.hk, pg, &full[stage]);
           }
         }
-        if (++stage == S::kStages) {
-          stage = 0;
+        if (++own == S::kOwnStages) {
+          own = 0;
           phase ^= 1;
         }
       }
       if (!ok) break;
+      turn = k - n;
       left -= n;
       tile = 0;
       if (left > 0) next_unit<kKeys>(p, u);
@@ -217,8 +223,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   Unit u = sh.u;
   int tile = sh.tile;
   int64_t left = sh.count, at = sh.begin;
-  int turn = 0;  // tiles handed out so far, modulo the warps
-  int stage = 0;
+  int turn = 0;      // tiles handed out so far, modulo the warps
+  int producer = 0;  // of the next tile, and which of its stages
+  int own = 0;
   uint32_t phase = 0;
   int parity = 0;
   bool ok = true;  // after a timeout the warps still meet at every barrier below
@@ -291,11 +298,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     for (int k = 0; k < n; ++k) {
       const bool mine = turn == warp;
       turn = turn + 1 == kDecWarps ? 0 : turn + 1;
-      const int st = stage;
+      const int st = producer * S::kOwnStages + own;
       const uint32_t ph = phase;
-      if (++stage == S::kStages) {
-        stage = 0;
-        phase ^= 1;
+      if (++producer == kDecProducers) {
+        producer = 0;
+        if (++own == S::kOwnStages) {
+          own = 0;
+          phase ^= 1;
+        }
       }
       if (!mine || !ok) continue;
       ok = __all_sync(0xffffffffu, mbar_wait(&full[st], ph));
