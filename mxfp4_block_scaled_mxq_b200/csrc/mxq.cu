@@ -451,47 +451,62 @@ struct PagedWorkspace {
   int64_t o = 0, ml = 0, units = 0, bytes = 0;
 };
 
-constexpr int kPagedMaxCtas = 160;  // at least the SMs of any sm_100 device; parts per unit < 4096
+constexpr int kPagedMaxCtas = 160;  // at least the SMs of any sm_100 device
+static_assert(kPagedMaxCtas * mxq::kDecWarps < 4096, "a unit's parts are counted in 12 bits");
 
-PagedWorkspace paged_workspace(int64_t rows, int64_t d) {
+PagedWorkspace paged_workspace(int tile_rows, int64_t d) {
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
+  const int64_t workers = kPagedMaxCtas * (tile_rows == mxq::kChunkRows ? 1 : mxq::kDecWarps);
   PagedWorkspace w;
-  w.ml = up(2 * kPagedMaxCtas * rows * d * 4);
-  w.units = w.ml + up(2 * kPagedMaxCtas * rows * 8);
-  w.bytes = w.units + up(kPagedMaxCtas * 16);
+  w.ml = up(2 * workers * tile_rows * d * 4);
+  w.units = w.ml + up(2 * workers * tile_rows * 8);
+  w.bytes = w.units + up(workers * 16);
   return w;
 }
 
-// Which kernel: the few-row one streams the cache once per 16 rows, the other computes 128 rows of
-// a tile whether they are there or not.  By the mean, since the lengths are on the device:
-// either kernel is right for any.
-bool paged_many_rows(int64_t T, int64_t batch, int64_t G) { return G <= mxq::kChunkHalf && T * G > 32 * batch; }
+// Which kernel, by the rows that share a key head: the few-row one streams the cache once per row tile
+// of 8, 16 or 32 rows, the other computes 256 whether they are there or not.  By the mean over the
+// sequences, since the lengths are on the device: every kernel is right for any.
+int paged_tile_rows(int64_t T, int64_t batch, int64_t G, int64_t d) {
+  const int64_t rows = (T * G + batch - 1) / batch;
+  if (rows <= 8) return 8;
+  if (rows <= 16) return 16;
+  if ((d == 64 && rows <= 32) || G > mxq::kChunkHalf) return d == 64 ? 32 : 16;
+  return mxq::kChunkRows;
+}
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-template <int D, int kRows>
-mxq_status launch_paged_join(const mxq::PagedParams& p, cudaStream_t stream) {
-  return launch_dependent(mxq::paged_join_kernel<D, kRows>, dim3(static_cast<unsigned>(p.ctas), kRows / 8), dim3(128),
-                          0, stream, p);
-}
-
-template <int D, bool kFp8>
+template <int D, bool kFp8, int kNt>
 mxq_status launch_paged_decode(const DeviceInfo& dev, const mxq_paged_kv* c, mxq::PagedParams p,
                                cudaStream_t stream) {
   using S = mxq::DecShape<D, kFp8>;
-  auto kernel = mxq::paged_decode_kernel<D, kFp8>;
+  auto kernel = mxq::paged_decode_kernel<D, kFp8, kNt>;
   static PerDevice setup;
   if (!setup.ensure(dev.index, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes) == cudaSuccess;
       }))
     return MXQ_ERR_CUDA;
-  p.tile_rows = mxq::kDecRows;
+  const int ctas = std::min(dev.sm_count, kPagedMaxCtas);
+  p.workers = ctas * mxq::kDecWarps;
   p.page_box = gcd(p.page_size, S::kKeys);
   CUtensorMap tk, tv;
   if (!make_tmap_cache(&tk, c, c->k, p.page_box) || !make_tmap_cache(&tv, c, c->v, p.page_box)) return MXQ_ERR_CUDA;
-  mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(mxq::kDecThreads), S::kSmemBytes,
+  mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), dim3(mxq::kDecThreads), S::kSmemBytes,
                                    stream, tk, tv, p);
-  return st != MXQ_OK ? st : launch_paged_join<D, mxq::kDecRows>(p, stream);
+  if (st != MXQ_OK) return st;
+  return launch_dependent(mxq::paged_join_few_kernel<D>,
+                          dim3(static_cast<unsigned>(p.workers), static_cast<unsigned>(std::min(p.G, 4))), dim3(256), 0,
+                          stream, p);
+}
+
+template <int D, bool kFp8>
+mxq_status launch_paged_few(const DeviceInfo& dev, const mxq_paged_kv* c, const mxq::PagedParams& p,
+                            cudaStream_t stream) {
+  if (p.tile_rows == 8) return launch_paged_decode<D, kFp8, 1>(dev, c, p, stream);
+  if constexpr (D == 64)
+    if (p.tile_rows == 32) return launch_paged_decode<D, kFp8, 4>(dev, c, p, stream);
+  return launch_paged_decode<D, kFp8, 2>(dev, c, p, stream);
 }
 
 // Q as (128-byte piece, piece, head, token): a box is one piece of the G heads of whole tokens.
@@ -520,6 +535,7 @@ mxq_status launch_paged_chunk(const DeviceInfo& dev, const mxq_paged_kv* c, mxq:
                cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes) == cudaSuccess;
       }))
     return MXQ_ERR_CUDA;
+  p.workers = std::min(dev.sm_count, kPagedMaxCtas);
   const int tokens = mxq::kChunkHalf / p.G;  // whole tokens of a half
   p.tile_rows = 2 * tokens * p.G;
   p.page_box = gcd(p.page_size, kFp8 ? S::kRawKeys : mxq::kChunkKeys);
@@ -527,9 +543,11 @@ mxq_status launch_paged_chunk(const DeviceInfo& dev, const mxq_paged_kv* c, mxq:
   if (!make_tmap_q(&tq, p, D, tokens) || !make_tmap_cache(&tk, c, c->k, p.page_box) ||
       !make_tmap_cache(&tv, c, c->v, p.page_box))
     return MXQ_ERR_CUDA;
-  mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(p.ctas)), dim3(S::kThreads), S::kSmemBytes,
+  mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(p.workers)), dim3(S::kThreads), S::kSmemBytes,
                                    stream, tq, tk, tv, p);
-  return st != MXQ_OK ? st : launch_paged_join<D, mxq::kChunkRows>(p, stream);
+  if (st != MXQ_OK) return st;
+  return launch_dependent(mxq::paged_join_many_kernel<D, mxq::kChunkRows>,
+                          dim3(static_cast<unsigned>(p.workers), mxq::kChunkRows / 8), dim3(2 * D), 0, stream, p);
 }
 
 }  // namespace
@@ -976,7 +994,7 @@ mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* cache, co
 
 int64_t mxq_attention_paged_workspace_bytes(int64_t T, int64_t batch, int64_t Hq, int64_t Hk, int64_t d) {
   if (T < 1 || batch < 1 || Hk < 1 || Hq < Hk || Hq % Hk != 0 || (d != 64 && d != 128)) return -1;
-  return paged_workspace(paged_many_rows(T, batch, Hq / Hk) ? mxq::kChunkRows : mxq::kDecRows, d).bytes;
+  return paged_workspace(paged_tile_rows(T, batch, Hq / Hk, d), d).bytes;
 }
 
 mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_t ldq, const mxq_paged_kv* cache,
@@ -996,8 +1014,8 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
   DeviceInfo dev;
   if ((st = current_device(&dev)) != MXQ_OK) return st;
 
-  const bool many = paged_many_rows(T, batch->batch, Hq / Hk);
-  const PagedWorkspace ws = paged_workspace(many ? mxq::kChunkRows : mxq::kDecRows, d);
+  const int tile_rows = paged_tile_rows(T, batch->batch, Hq / Hk, d);
+  const PagedWorkspace ws = paged_workspace(tile_rows, d);
   auto* base = static_cast<uint8_t*>(workspace);
   mxq::PagedParams p = {};
   p.q = static_cast<const uint16_t*>(q_bf16);
@@ -1020,11 +1038,11 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
   p.out32 = ldo % 16 == 0 && aligned(out_bf16, 32);  // and d % 16 == 0
   p.causal = causal != 0;
   p.window = static_cast<int>(window);
-  p.ctas = std::min(dev.sm_count, kPagedMaxCtas);
+  p.tile_rows = tile_rows;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
   p.v_scale = cache->v_scale;
   const bool fp8 = cache->fmt == MXQ_KV_FP8_E4M3;
-  if (many) {
+  if (tile_rows == mxq::kChunkRows) {
     if (d == 128)
       return fp8 ? launch_paged_chunk<128, true>(dev, cache, p, stream)
                  : launch_paged_chunk<128, false>(dev, cache, p, stream);
@@ -1032,10 +1050,8 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
                : launch_paged_chunk<64, false>(dev, cache, p, stream);
   }
   if (d == 128)
-    return fp8 ? launch_paged_decode<128, true>(dev, cache, p, stream)
-               : launch_paged_decode<128, false>(dev, cache, p, stream);
-  return fp8 ? launch_paged_decode<64, true>(dev, cache, p, stream)
-             : launch_paged_decode<64, false>(dev, cache, p, stream);
+    return fp8 ? launch_paged_few<128, true>(dev, cache, p, stream) : launch_paged_few<128, false>(dev, cache, p, stream);
+  return fp8 ? launch_paged_few<64, true>(dev, cache, p, stream) : launch_paged_few<64, false>(dev, cache, p, stream);
 }
 
 mxq_status mxq_selftest_wait_timeout(mxq_stream_t stream) {

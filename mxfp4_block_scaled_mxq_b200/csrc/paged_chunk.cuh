@@ -154,7 +154,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
   }
   griddep_launch_dependents();
   griddep_wait();
-  const Share sh = find_share<kChunkKeys, S::kThreads, kChunkMinTiles>(p, scratch);
+  const Share sh = find_share<kChunkKeys, S::kThreads, 1, kChunkMinTiles>(p, scratch);
   if (tid == 0 && sh.count == 0) p.part_units[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
@@ -668,11 +668,8 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           tc_fence_before();
         }
       }
-      if (tid == 0 && left == n) {
-        int parts = 0;
-        if (tile == 0 && n < u.nt) parts = owner(sh, at + u.nt - 1) - static_cast<int>(blockIdx.x) + 1;
-        p.part_units[blockIdx.x] = make_int4(static_cast<int>(u.s.q0), u.rt, u.rows, u.hk * 4096 + parts);
-      }
+      if (tid == 0 && left == n)
+        p.part_units[blockIdx.x] = part_unit(sh, u, static_cast<int>(blockIdx.x), at, tile == 0 && n < u.nt);
       g += n;
       ++units;
       left -= n;

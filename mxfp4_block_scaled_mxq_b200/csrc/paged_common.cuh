@@ -8,12 +8,12 @@
 //
 // Work.  The query heads of one key head share its keys, so a row is (token, head of the group)
 // and a unit is (sequence, key head, row tile) with the key tiles its rows reach.  All units'
-// key tiles in a line, every CTA takes an equal, contiguous share of it: the load is even
-// whatever the lengths, nothing is planned on the host, and only the first and the last
-// segment of a CTA can be a part of a unit.  Such a part goes to the workspace as an
-// unnormalised FP32 accumulator with its row maxima and sums (two slots per CTA, so the
-// workspace does not grow with the lengths), and the joining kernel adds the parts of each unit
-// in the order of the keys.
+// key tiles in a line, every worker (a CTA, or a warp in the few-row kernel) takes an equal,
+// contiguous share of it: the load is even whatever the lengths, nothing is planned on the host,
+// and only the first and the last segment of a share can be a part of a unit.  Such a part goes
+// to the workspace as an unnormalised FP32 accumulator with its row maxima and sums (two
+// slots per worker, so the workspace does not grow with the lengths), and the joining kernel
+// adds the parts of each unit in the order of the keys.
 #pragma once
 
 #include "gemm_common.cuh"
@@ -26,9 +26,9 @@ struct PagedParams {
   const int32_t* cu_q;
   const int32_t* kv_len;
   const int32_t* block_table;
-  float* part_o;     // [2 ctas][d / 4][rows][4]
-  float2* part_ml;   // [2 ctas][rows]: (row maximum, row sum)
-  int4* part_units;  // [ctas]: the unit that CTA c begins and does not finish: (the sequence's first
+  float* part_o;     // [2 workers][rows x d]
+  float2* part_ml;   // [2 workers][rows]: (row maximum, row sum)
+  int4* part_units;  // [workers]: the unit that a worker begins and does not finish: (the sequence's first
                      // row of Q, row tile, rows in it, key head * 4096 + parts); parts 0: none
   int64_t ldq, ldo, T, table_stride;
   int batch, num_pages, page_size;
@@ -37,7 +37,7 @@ struct PagedParams {
   int causal, window;  // window 0: none
   int out32;           // rows of `out` are 32-byte aligned
   int page_box;        // keys per TMA box: gcd(page size, key tile)
-  int ctas;            // that share the work (the partial slots' count is twice that)
+  int workers;         // that may share the work
   float scale_log2;    // scale * log2(e) * k_scale
   float v_scale;
 };
@@ -124,32 +124,36 @@ __device__ __forceinline__ void next_unit(const PagedParams& p, Unit& u) {
   set_unit<kKeys>(p, u);
 }
 
-// This CTA's share of the line: where it begins, and how many key tiles it has.
+// A worker's share of the line: where it begins, and how many key tiles it has.
 struct Share {
   Unit u;
   int tile;              // first key tile within the unit
   int64_t begin, count;  // key tiles: the first one's place in the line, how many
   int64_t total;         // the line's length
-  int shares;            // CTAs that have one
+  int shares;            // workers that have one
 };
+
+constexpr int kMaxWorkers = 16;  // of one CTA
 
 struct ShareScratch {
   int64_t warp_sum[32];
-  int64_t weight, rest;
-  int b;
+  int64_t weight[kMaxWorkers], rest[kMaxWorkers];
+  int b[kMaxWorkers];
 };
 
-// Called by all kThreads threads.  Sequences are weighed in parallel, by a warp each when
-// there are few of them (a long chunk has many row tiles), by a thread each otherwise.  A
-// share has at least about kMinTiles key tiles: fewer CTAs take part in a small call.
-template <int kKeys, int kThreads, int kMinTiles>
+// The share of this thread's worker: the CTA has kWorkers, one for each of its first kWorkers
+// warps (or one for all of them).  Called by all kThreads threads.  Sequences are weighed in
+// parallel, by a warp each when there are few of them (a long chunk has many row tiles), by a
+// thread each otherwise.  A share has at least about kMinTiles key tiles: fewer workers take part in
+// a small call.
+template <int kKeys, int kThreads, int kWorkers, int kMinTiles>
 __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& sc) {
   constexpr int kWarps = kThreads / 32;
-  static_assert(kWarps <= 32, "scratch");
+  static_assert(kWarps <= 32 && kWorkers <= kMaxWorkers && kWorkers <= kWarps, "scratch");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool by_warp = p.batch <= kWarps;
   const int per_round = by_warp ? kWarps : kThreads;
-  auto weigh = [&](int b) -> int64_t {  // by_warp: the same value in lane 0 only, 0 elsewhere
+  auto weigh = [&](int b) -> int64_t {  // by_warp: in lane 0 only, 0 elsewhere
     int64_t w = 0;
     if (b < p.batch) {
       const Sequence s = load_sequence(p, b);
@@ -164,7 +168,6 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
     }
     return w;
   };
-  if (tid == 0) sc.b = -1;
   int64_t total = 0, mine = 0;
   const int rounds = (p.batch + per_round - 1) / per_round;
   // the total, then (with the weights still in hand when one round holds them all) the search
@@ -174,13 +177,13 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
     for (int m = 16; m > 0; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
     __syncthreads();
     if (lane == 0) sc.warp_sum[warp] = w;
+    if (tid < kWorkers) sc.b[tid] = -1;
     __syncthreads();
     for (int i = 0; i < kWarps; ++i) total += sc.warp_sum[i];
   }
-  const int64_t c = blockIdx.x;
-  const int64_t shares = min(static_cast<int64_t>(p.ctas), (total + kMinTiles - 1) / kMinTiles);
-  const int64_t begin = c < shares ? total * c / shares : total;
-  const int64_t end = c < shares ? total * (c + 1) / shares : total;
+  const int64_t shares = min(static_cast<int64_t>(p.workers), (total + kMinTiles - 1) / kMinTiles);
+  auto bound = [&](int64_t c) { return c < shares ? total * c / shares : total; };
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kWorkers;
   int64_t before = 0;
   for (int r = 0; r < rounds; ++r) {
     const int b = r * per_round + (by_warp ? warp : tid);
@@ -195,28 +198,35 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
       if (lane == 31) sc.warp_sum[warp] = incl;
       __syncthreads();
     }  // one round: the first loop's sums are these
-    int64_t base = before;
-    for (int i = 0; i < warp; ++i) base += sc.warp_sum[i];
-    const int64_t lo = base + incl - mine;
-    if (mine > 0 && lo <= begin && begin < lo + mine) {
-      sc.b = b;
-      sc.rest = begin - lo;
-      sc.weight = mine;
+    int64_t lo = before + incl - mine;
+    for (int i = 0; i < warp; ++i) lo += sc.warp_sum[i];
+    if (mine > 0) {
+      // the first worker of this CTA whose share begins at or after lo: shares are in order
+      for (int w = 0; w < kWorkers; ++w) {
+        const int64_t begin = bound(c0 + w);
+        if (begin >= lo + mine) break;
+        if (begin >= lo) {
+          sc.b[w] = b;
+          sc.rest[w] = begin - lo;
+          sc.weight[w] = mine;
+        }
+      }
     }
     for (int i = 0; i < kWarps; ++i) before += sc.warp_sum[i];
   }
   __syncthreads();
+  const int worker = kWorkers == 1 ? 0 : min(warp, kWorkers - 1);
   Share sh;
-  sh.begin = begin;
-  sh.count = sc.b < 0 ? 0 : end - begin;
+  sh.begin = bound(c0 + worker);
+  sh.count = sc.b[worker] < 0 ? 0 : bound(c0 + worker + 1) - sh.begin;
   sh.total = total;
   sh.shares = static_cast<int>(shares);
   sh.tile = 0;
-  sh.u.b = sc.b;
+  sh.u.b = sc.b[worker];
   if (sh.count > 0) {
     sh.u.s = load_sequence(p, sh.u.b);
-    const int64_t per_head = sc.weight / p.Hk;
-    int64_t rest = sc.rest;
+    const int64_t per_head = sc.weight[worker] / p.Hk;
+    int64_t rest = sc.rest[worker];
     sh.u.hk = static_cast<int>(rest / per_head);
     rest -= sh.u.hk * per_head;
     // the row tile: 32 at a time, each warp for itself
@@ -242,7 +252,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
   return sh;
 }
 
-// The CTA that has the key tile at place x of the line.
+// The worker that has the key tile at place x of the line.
 __device__ __forceinline__ int owner(const Share& sh, int64_t x) {
   return static_cast<int>(((x + 1) * sh.shares - 1) / sh.total);
 }
@@ -254,13 +264,76 @@ __device__ __forceinline__ int64_t row_offset(const PagedParams& p, int64_t q0, 
   return (q0 + i) * ld + static_cast<int64_t>(hk * p.G + r - i * p.G) * D;
 }
 
-// Joins the parts of the unit that CTA blockIdx.x began: its last slot, then the first slots
-// of the CTAs after it.  A block has 8 rows x 16 groups of D / 16 columns: the parts' loads are
-// consecutive over the rows, the result's over the columns.
+// What worker c leaves for the joining kernel: parts 0 unless it began the unit and did not
+// finish it.  `at`: the place in the line of its first tile in the unit.
+__device__ __forceinline__ int4 part_unit(const Share& sh, const Unit& u, int c, int64_t at, bool begun_only) {
+  const int parts = begun_only ? owner(sh, at + u.nt - 1) - c + 1 : 0;
+  return make_int4(static_cast<int>(u.s.q0), u.rt, u.rows, u.hk * 4096 + parts);
+}
+
+// Joins the parts of the unit that worker blockIdx.x began: its last slot, then the first slots of
+// the workers after it.  Few rows: a block has one row at a time, groups of four columns times
+// 256 / (D / 4) slices of the parts (a unit that spans the whole machine has over a thousand).
+// The maximum of the parts' row maxima, and the NaN of any of them.
+__device__ __forceinline__ float max_or_nan(float a, float b) { return a != a || a >= b ? a : b; }
+
+template <int D>
+__global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p) {
+  constexpr int kGroups = D / 4, kSlices = 256 / kGroups;
+  __shared__ float s_m[8], s_l[kSlices];
+  __shared__ float4 s_o[kSlices][kGroups];
+  griddep_wait();
+  const int c = blockIdx.x;
+  const int4 un = p.part_units[c];
+  const int parts = un.w & 4095;
+  if (parts == 0) return;
+  const int lane = threadIdx.x & 31, group = threadIdx.x % kGroups, slice = threadIdx.x / kGroups;
+  auto row_of = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.tile_rows + r; };
+  for (int r = blockIdx.y; r < un.z; r += gridDim.y) {
+    float m = -INFINITY;
+    for (int i = threadIdx.x; i < parts; i += 256) m = max_or_nan(m, p.part_ml[row_of(i, r)].x);
+    for (int k = 16; k > 0; k >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
+    if (lane == 0) s_m[threadIdx.x >> 5] = m;
+    __syncthreads();
+    for (int i = 0; i < 8; ++i) m = max_or_nan(m, s_m[i]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int i = slice; i < parts; i += kSlices) {
+      const float2 ml = p.part_ml[row_of(i, r)];
+      const float f = exp2f(ml.x - base);
+      l = fmaf(ml.y, f, l);
+      const float4 v = reinterpret_cast<const float4*>(p.part_o)[row_of(i, r) * kGroups + group];
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
+    }
+    s_o[slice][group] = acc;
+    if (group == 0) s_l[slice] = l;
+    __syncthreads();
+    if (slice == 0) {
+      for (int i = 1; i < kSlices; ++i) {
+        const float4 v = s_o[i][group];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        l += s_l[i];
+      }
+      const float inv = l == 0.f ? 0.f : p.v_scale / l;
+      uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + 4 * group;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+    __syncthreads();
+  }
+}
+
+// Many rows: a block has 8 rows and all groups of four columns; parts are [d / 4][row][4], the
+// layout in which the thread per row that wrote them stored consecutively.
 template <int D, int kRows>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p) {
-  constexpr int kGroup = D / 16;   // columns of a thread
-  constexpr int kVec = kGroup / 4;
+__global__ void __launch_bounds__(2 * D) paged_join_many_kernel(const PagedParams p) {
   griddep_wait();
   const int c = blockIdx.x;
   const int4 un = p.part_units[c];
@@ -269,30 +342,25 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedParams p) {
   if (parts == 0 || r >= un.z) return;
   auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)); };
   float m = -INFINITY;
-  for (int i = 0; i < parts; ++i) m = fmaxf(m, p.part_ml[slot(i) * kRows + r].x);
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) m = max_or_nan(m, p.part_ml[slot(i) * kRows + r].x);
   const float base = m == -INFINITY ? 0.f : m;
-  float acc[kGroup] = {}, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
 #pragma unroll 4
   for (int i = 0; i < parts; ++i) {
     const float2 ml = p.part_ml[slot(i) * kRows + r];
     const float f = exp2f(ml.x - base);
     l = fmaf(ml.y, f, l);
-    const float4* o = reinterpret_cast<const float4*>(p.part_o) + (slot(i) * (D / 4) + group * kVec) * kRows + r;
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      const float4 v = o[k * kRows];
-      acc[4 * k] = fmaf(v.x, f, acc[4 * k]);
-      acc[4 * k + 1] = fmaf(v.y, f, acc[4 * k + 1]);
-      acc[4 * k + 2] = fmaf(v.z, f, acc[4 * k + 2]);
-      acc[4 * k + 3] = fmaf(v.w, f, acc[4 * k + 3]);
-    }
+    const float4 v = reinterpret_cast<const float4*>(p.part_o)[(slot(i) * (D / 4) + group) * kRows + r];
+    acc.x = fmaf(v.x, f, acc.x);
+    acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z);
+    acc.w = fmaf(v.w, f, acc.w);
   }
   const float inv = l == 0.f ? 0.f : p.v_scale / l;
-  uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + group * kGroup;
-#pragma unroll
-  for (int k = 0; k < kVec; ++k)
-    *reinterpret_cast<uint2*>(dst + 4 * k) = make_uint2(pack_bf16x2(acc[4 * k] * inv, acc[4 * k + 1] * inv),
-                                                        pack_bf16x2(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
+  uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + 4 * group;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 }  // namespace mxq

@@ -1,21 +1,26 @@
 // paged_decode.cuh -- attention of few rows (generated or drafted tokens) over a paged cache.
 //
 // The cache is read once and little is computed on it, so this kernel is bound by DRAM.  One
-// CTA per SM: producer warps keep a ring of key tiles (K and V of kKeys keys, TMA boxes of one
-// page each, zero fill for pages that are missing) full in shared memory, up to 180 KB in
-// flight, across units; eight consumer warps take the tiles in turn.  Four producer warps, since
-// one needs about 1000 cycles for a tile's pages and copies and 16 KB a tile have to come every 700.  A warp holds 16 rows
-// and its own running maximum, sum and accumulator, so nothing is exchanged per tile: scores
-// by mma.sync m16n8k16 (the rows are too few for a tcgen05 tile of 128), one online-softmax
-// step in base 2, then P V with P in registers.  At the end of a unit the eight warps' states
-// are joined through shared memory.
+// CTA of eight warps per SM, and every warp a worker of its own: it has its share of the key tiles,
+// keeps its ring of three tiles (8 KB of K and V each: 192 KB in flight per SM; TMA boxes of
+// one page, zero fill for pages that are missing) full across units, and holds 8, 16 or 32 rows'
+// running maxima, sums and accumulators.  Nothing is exchanged between warps, so a change of unit
+// costs one warp's latency under the seven others' loads (with the CTA as the worker and the
+// warps joined at the end of each unit it cost 4 us of the SM).
+//
+// The products are taken transposed, S^T = K Q^T and O^T = V^T P^T, by mma.sync m16n8k16 with the
+// cache as the 16-row operand and the rows as the 8 columns: a group of up to 8 heads wastes
+// nothing (as the 16-row operand it would waste half of every product and of the softmax; a tcgen05 tile
+// of 128 rows nearly all).  P goes from the one accumulator layout to the other operand's by
+// transposing its 8 x 8 blocks (movmatrix).  The running maximum is raised lazily, by more than 8
+// in base 2, so that a tile usually needs no reduction across lanes and no rescaling.
 //
 // BF16 cache: operands by ldmatrix from the 128-byte-swizzled tiles, P rounded to BF16.
 // E4M3 cache: K and V are converted to FP16, which holds E4M3 exactly; Q is scaled per row by
 // a power of two into FP16 (11 bits, exact for BF16's 8 down to 2^-14 of the row's largest
-// value) and P is rounded to FP16.  The order of the head dimension in the
-// first product and of the output columns in the second is free, so each lane takes
-// contiguous bytes of K rows (16) and V rows (D / 8) and no byte is shuffled across lanes.
+// value) and P is rounded to FP16.  The order of the head dimension in the first product and of the
+// output columns in the second is free, so each lane takes contiguous bytes of K rows (16) and
+// V rows (D / 8) and no byte is shuffled across lanes.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -24,32 +29,21 @@
 
 namespace mxq {
 
-constexpr int kDecRows = 16;
 constexpr int kDecWarps = 8;
-constexpr int kDecProducers = 4;
-constexpr int kDecThreads = 32 * (kDecWarps + kDecProducers);
-constexpr int kDecMaxStages = 24;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecStages = 3;  // of each warp
+constexpr int kDecStageBytes = 8192;
 constexpr int kDecMinTiles = 4;
 
 template <int D, bool kFp8>
 struct DecShape {
-  static constexpr int kKeys = kFp8 ? 64 : 32;
   static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
-  static constexpr int kTileBytes = kKeys * kRowBytes;  // K or V
-  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kTileBytes = kDecStageBytes / 2;  // K or V
+  static constexpr int kKeys = kTileBytes / kRowBytes;
   static constexpr int kBoxRowBytes = kRowBytes > 128 ? 128 : kRowBytes;  // one TMA box's row
   static constexpr int kHalves = kRowBytes / kBoxRowBytes;
-  static constexpr int kMergeBytes = kDecWarps / 2 * kDecRows * D * 4;
-  static constexpr int kMlBytes = 2 * kDecWarps * kDecRows * 8;
-  static constexpr int kFixed = 1024 + kMergeBytes + kMlBytes + kDecMaxStages * 20 + 512;
-  static constexpr int kFit = (225 * 1024 - kFixed) / kStageBytes;
-  // A stage is always filled by the same producer warp and read by the same consumer warp, each in
-  // order: a warp that met the stage of another could be two rounds from it, where a barrier's
-  // parity says nothing.
-  static constexpr int kStages = (kFit < kDecMaxStages ? kFit : kDecMaxStages) / kDecWarps * kDecWarps;
-  static constexpr int kOwnStages = kStages / kDecProducers;
-  static_assert(kStages >= kDecWarps && kDecWarps % kDecProducers == 0, "stages");
-  static constexpr int kSmemBytes = kFixed + kStages * kStageBytes;
+  static constexpr int kSmemBytes = 1024 + kDecWarps * kDecStages * kDecStageBytes;
+  static_assert(kKeys >= 16 && kKeys / 8 * kHalves * 2 <= 32, "a lane for each copy");
 };
 
 __device__ __forceinline__ void tma_load_5d(void* smem_dst, const CUtensorMap* m, int32_t c0, int32_t c1, int32_t c2,
@@ -95,6 +89,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The 8 x 8 block of 16-bit values of which each lane holds two of a row, transposed.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // E4M3 pairs (bits 0-15, 16-31) -> FP16 pairs, exactly.
 __device__ __forceinline__ uint2 e4m3x4_to_f16(uint32_t w) {
   uint2 h;
@@ -110,209 +111,161 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ void bar_consumers() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kDecWarps) : "memory");
-}
-
-template <int D, bool kFp8>
+// kNt: blocks of eight rows of a unit.
+template <int D, bool kFp8, int kNt>
 __global__ void __launch_bounds__(kDecThreads, 1)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         const PagedParams p) {
   using S = DecShape<D, kFp8>;
   constexpr int kKeys = S::kKeys;
-  constexpr int kNt = kKeys / 8;   // score tiles of 8 keys
-  constexpr int kKs = D / 16;      // steps of the first product
-  constexpr int kOt = D / 8;       // output tiles of 8 columns
+  constexpr int kMt = kKeys / 16;  // blocks of 16 keys
+  constexpr int kKs = D / 16;      // steps of the first product, blocks of 16 output columns
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* ring = smem;
-  float* merge = reinterpret_cast<float*>(smem + S::kStages * S::kStageBytes);
-  float2* ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(merge) + S::kMergeBytes);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ml) + S::kMlBytes);
-  uint64_t* empty = full + kDecMaxStages;
-  uint32_t* boxes = reinterpret_cast<uint32_t*>(empty + kDecMaxStages);  // per stage: boxes that hold a page
   __shared__ ShareScratch scratch;
+  __shared__ uint64_t full_bars[kDecWarps][kDecStages];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
-    for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
+    for (int s = 0; s < kDecWarps * kDecStages; ++s) mbar_init(&full_bars[0][0] + s, 1);
     fence_mbar_init();
   }
   griddep_launch_dependents();
   griddep_wait();
-  const Share sh = find_share<kKeys, kDecThreads, kDecMinTiles>(p, scratch);  // has the block's barriers
-  if (tid == 0 && sh.count == 0) p.part_units[blockIdx.x] = make_int4(0, 0, 0, 0);
-  __syncthreads();
+  const Share sh = find_share<kKeys, kDecThreads, kDecWarps, kDecMinTiles>(p, scratch);  // has the block's barriers
+  const int worker = blockIdx.x * kDecWarps + warp;
+  if (lane == 0) p.part_units[worker] = make_int4(0, 0, 0, 0);
   if (sh.count == 0) return;
+  uint8_t* ring = smem + warp * kDecStages * kDecStageBytes;
+  uint64_t* full = full_bars[warp];
 
-  if (warp >= kDecWarps) {
-    // ------------------------------------------------------------------ producers
-    Unit u = sh.u;
-    int tile = sh.tile;
-    const int nbox = kKeys / p.page_box;
-    int own = 0;                  // this warp's next stage among its own
-    int turn = warp - kDecWarps;  // tiles until its next one
-    uint32_t phase = 0;
-    bool ok = true;
-    int64_t left = sh.count;
-    uint32_t issued = 0, issued_phase = 0;
-    int batch_at = -1, batch_b = -1, entries = -1;  // block-table entries [batch_at, +32) of sequence batch_b
-    while (ok && left > 0) {
-      const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
-      const int32_t* table = p.block_table + static_cast<int64_t>(u.b) * p.table_stride;
-      int k = turn;
-      for (; k < n; k += kDecProducers) {
-        const int stage = (warp - kDecWarps) * S::kOwnStages + own;
-        const int key0 = (u.kt0 + tile + k) * kKeys;
-        // pages of the tile's boxes: lane i < nbox has box i
-        const int box_key = key0 + lane * p.page_box;
-        const int first = key0 / p.page_size, entry = box_key / p.page_size;
-        if (batch_b != u.b || first < batch_at || first + nbox > batch_at + 32) {
-          batch_b = u.b;
-          batch_at = first;
-          entries = first + lane < p.table_stride ? table[first + lane] : -1;
-        }
-        const int page = __shfl_sync(0xffffffffu, entries, min(entry - batch_at, 31));
-        const bool need = lane < nbox && box_key < u.hi && box_key + p.page_box > u.lo;
-        const bool there = need && page >= 0 && page < p.num_pages;
-        const uint32_t mask = __ballot_sync(0xffffffffu, there);
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1));
-        if (!ok) break;
-        issued |= 1u << stage;
-        issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
-        if (lane == 0) {
-          boxes[stage] = mask;
-          mbar_arrive_expect_tx(&full[stage], S::kStageBytes);
-        }
-        __syncwarp();
-        if (lane < nbox) {
-          const int pg = there ? page : -1;  // out of range: the box is filled with zeros
-          const int in_page = there ? box_key - entry * p.page_size : 0;
-          uint8_t* dst = ring + stage * S::kStageBytes + lane * p.page_box * S::kBoxRowBytes;
+  // Copies run kDecStages tiles ahead of the tile at hand.  Lane i has copy i of a tile: K or V, the
+  // 128-byte piece, the box.
+  const int nbox = kKeys / p.page_box, box_shift = 31 - __clz(p.page_box);
+  const int box = lane % nbox, piece = lane / nbox % S::kHalves;
+  const bool is_v = lane >= nbox * S::kHalves, copies = lane < nbox * S::kHalves * 2;
+  Unit lu = sh.u;
+  int ltile = sh.tile;
+  int64_t lleft = sh.count;
+  int batch_at = 0, batch_b = -1, entries = -1;  // block-table entries [batch_at, +32) of sequence batch_b
+  uint32_t boxes[kDecStages] = {};               // per stage: boxes whose page is there
+  auto copy_next = [&](int stage) {
+    if (lleft == 0) return;
+    const int key0 = (lu.kt0 + ltile) * kKeys;
+    const int first = key0 / p.page_size, box_key = key0 + box * p.page_box, entry = box_key / p.page_size;
+    if (batch_b != lu.b || first < batch_at || first + nbox > batch_at + 32) {
+      batch_b = lu.b;
+      batch_at = first;
+      entries = first + lane < p.table_stride ? p.block_table[lu.b * p.table_stride + first + lane] : -1;
+    }
+    const int page = __shfl_sync(0xffffffffu, entries, min(entry - batch_at, 31));
+    const bool need = box_key < lu.hi && box_key + p.page_box > lu.lo;
+    const bool there = need && page >= 0 && page < p.num_pages;
+    const uint32_t mask = __ballot_sync(0xffffffffu, lane < nbox && there);
 #pragma unroll
-          for (int h = 0; h < S::kHalves; ++h) {
-            tma_load_5d(dst + h * kKeys * 128, &tmap_k, 0, in_page, h, u.hk, pg, &full[stage]);
-            tma_load_5d(dst + S::kTileBytes + h * kKeys * 128, &tmap_v, 0, in_page, h, u.hk, pg, &full[stage]);
-          }
-        }
-        if (++own == S::kOwnStages) {
-          own = 0;
-          phase ^= 1;
-        }
-      }
-      if (!ok) break;
-      turn = k - n;
-      left -= n;
-      tile = 0;
-      if (left > 0) next_unit<kKeys>(p, u);
+    for (int s = 0; s < kDecStages; ++s)
+      if (s == stage) boxes[s] = mask;
+    if (lane == 0) mbar_arrive_expect_tx(&full[stage], kDecStageBytes);
+    __syncwarp();
+    if (copies) {
+      uint8_t* dst = ring + stage * kDecStageBytes + (is_v ? S::kTileBytes : 0) + piece * kKeys * 128 +
+                     box * p.page_box * S::kBoxRowBytes;
+      tma_load_5d(dst, is_v ? &tmap_v : &tmap_k, 0, there ? box_key - entry * p.page_size : 0, piece, lu.hk,
+                  there ? page : -1, &full[stage]);  // page out of range: the box is filled with zeros
     }
-    if (!ok) {
-      for (int s = 0; s < S::kStages; ++s)
-        if (issued & (1u << s)) mbar_wait_drain(&full[s], (issued_phase >> s) & 1u);
+    --lleft;
+    if (++ltile == lu.nt && lleft > 0) {
+      next_unit<kKeys>(p, lu);
+      ltile = 0;
+      // its queries, which are wanted when it begins
+      if (lane < lu.rows)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + row_offset<D>(p, lu.s.q0, lu.hk, lu.r0 + lane, p.ldq)));
     }
-    return;
-  }
+  };
+  for (int s = 0; s < kDecStages; ++s) copy_next(s);
 
-  // -------------------------------------------------------------------- consumers
-  const int r = lane >> 2, c = lane & 3;  // rows r and r + 8; column pair c
+  // Fragments: lane (r, c) has row r (of eight) of a block as an operand, and rows 2 c, 2 c + 1 in
+  // accumulators.
+  const int r = lane >> 2, c = lane & 3;
   Unit u = sh.u;
   int tile = sh.tile;
   int64_t left = sh.count, at = sh.begin;
-  int turn = 0;      // tiles handed out so far, modulo the warps
-  int producer = 0;  // of the next tile, and which of its stages
-  int own = 0;
+  int st = 0;
   uint32_t phase = 0;
-  int parity = 0;
-  bool ok = true;  // after a timeout the warps still meet at every barrier below
-  while (left > 0) {
+  bool ok = true;
+  while (ok && left > 0) {
     const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
-    // Q fragments of rows r, r + 8, and the keys they attend
-    uint32_t qa[kKs][4];
-    float t_scale[2];
-    int klo[2], khi[2];
-    {
-      const uint16_t* src[2];
+    uint32_t qb[kKs][kNt][2];
+    float t_scale[kNt][2];
+    int klo[kNt][2], khi[kNt][2];  // the keys that rows 8 t + 2 c, + 1 attend
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = u.r0 + min(r + 8 * i, u.rows - 1);
-        src[i] = p.q + row_offset<D>(p, u.s.q0, u.hk, row, p.ldq);
-        const int2 kr = key_range(p, u.s, row / p.G, row / p.G);
-        klo[i] = kr.x;
-        khi[i] = kr.y;
-        t_scale[i] = p.scale_log2;
-      }
+    for (int t = 0; t < kNt; ++t) {
+      const uint16_t* src = p.q + row_offset<D>(p, u.s.q0, u.hk, u.r0 + min(8 * t + r, u.rows - 1), p.ldq);
       if constexpr (kFp8) {
-        uint2 raw[2][kKs];
+        uint2 raw[kKs];
+        float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int s = 0; s < kKs; ++s) raw[s] = *reinterpret_cast<const uint2*>(src + (s >> 2) * 64 + 16 * c + 4 * (s & 3));
 #pragma unroll
-          for (int s = 0; s < kKs; ++s)
-            raw[i][s] = *reinterpret_cast<const uint2*>(src[i] + (s >> 2) * 64 + 16 * c + 4 * (s & 3));
+        for (int s = 0; s < kKs; ++s) {
+          const uint32_t w[2] = {raw[s].x, raw[s].y};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float big = 0.f;
-#pragma unroll
-          for (int s = 0; s < kKs; ++s) {
-            const uint32_t w[2] = {raw[i][s].x, raw[i][s].y};
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
-          }
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          // 2^-e with the row's largest value in [1, 2) 2^e; rows outside |e| <= 100 are left as they are
-          const int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-          const bool fits = e >= -100 && e <= 100;
-          const float down = fits ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
-          t_scale[i] = fits ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : p.scale_log2;
-#pragma unroll
-          for (int s = 0; s < kKs; ++s) {
-            const uint32_t w[2] = {raw[i][s].x, raw[i][s].y};
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              qa[s][i + 2 * k] = pack_f16x2(__uint_as_float(w[k] << 16) * down,
-                                            __uint_as_float(w[k] & 0xffff0000u) * down);
-          }
+          for (int k = 0; k < 2; ++k)
+            big = fmaxf(big, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xffff0000u))));
         }
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^-e with the row's largest value in [1, 2) 2^e; rows outside |e| <= 100 are left as they are
+        const int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
+        const bool fits = e >= -100 && e <= 100;
+        const float down = fits ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
+        const float up = fits ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : p.scale_log2;
+#pragma unroll
+        for (int s = 0; s < kKs; ++s) {
+          const uint32_t w[2] = {raw[s].x, raw[s].y};
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            qb[s][t][k] = pack_f16x2(__uint_as_float(w[k] << 16) * down, __uint_as_float(w[k] & 0xffff0000u) * down);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) t_scale[t][i] = __shfl_sync(0xffffffffu, up, 4 * (2 * c + i));
       } else {
 #pragma unroll
         for (int s = 0; s < kKs; ++s)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            qa[s][i] = *reinterpret_cast<const uint32_t*>(src[i] + 16 * s + 2 * c);
-            qa[s][i + 2] = *reinterpret_cast<const uint32_t*>(src[i] + 16 * s + 8 + 2 * c);
-          }
+          for (int k = 0; k < 2; ++k) qb[s][t][k] = *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 * k + 2 * c);
+        t_scale[t][0] = t_scale[t][1] = p.scale_log2;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int tok = (u.r0 + min(8 * t + 2 * c + i, u.rows - 1)) / p.G;
+        const int2 kr = key_range(p, u.s, tok, tok);
+        klo[t][i] = kr.x;
+        khi[t][i] = kr.y;
       }
     }
     // keys that every row of the tile attends
     const int all_lo = key_range(p, u.s, u.i1, u.i1).x, all_hi = key_range(p, u.s, u.i0, u.i0).y;
-    const uint32_t all_boxes = (kKeys / p.page_box) == 32 ? 0xffffffffu : (1u << (kKeys / p.page_box)) - 1u;
+    const uint32_t all_boxes = (1u << nbox) - 1u;
 
-    float o[kOt][4] = {};
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[kKs][kNt][4] = {};
+    float m[kNt][2], l[kNt][2];
+#pragma unroll
+    for (int t = 0; t < kNt; ++t) {
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+    }
     for (int k = 0; k < n; ++k) {
-      const bool mine = turn == warp;
-      turn = turn + 1 == kDecWarps ? 0 : turn + 1;
-      const int st = producer * S::kOwnStages + own;
-      const uint32_t ph = phase;
-      if (++producer == kDecProducers) {
-        producer = 0;
-        if (++own == S::kOwnStages) {
-          own = 0;
-          phase ^= 1;
-        }
-      }
-      if (!mine || !ok) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait(&full[st], ph));
-      if (!ok) continue;  // timed out: the status word is set and every other wait gives up too
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[st], phase));
+      if (!ok) break;
       const int key0 = (u.kt0 + tile + k) * kKeys;
-      const uint32_t there = boxes[st];
-      uint8_t* kt = ring + st * S::kStageBytes;
+      uint32_t there = boxes[0];
+#pragma unroll
+      for (int s = 1; s < kDecStages; ++s)
+        if (s == st) there = boxes[s];
+      uint8_t* kt = ring + st * kDecStageBytes;
       uint8_t* vt = kt + S::kTileBytes;
       const uint32_t ks = smem_u32(kt), vs = smem_u32(vt);
       if (key0 < u.lo || key0 + kKeys > u.hi) {
@@ -327,92 +280,113 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         __syncwarp();
       }
-      // S = Q K^T
-      float sc[kNt][4];
+      // S^T = K Q^T
+      float sc[kMt][kNt][4];
 #pragma unroll
-      for (int t = 0; t < kNt; ++t) {
-        sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+      for (int mt = 0; mt < kMt; ++mt) {
+#pragma unroll
+        for (int t = 0; t < kNt; ++t) sc[mt][t][0] = sc[mt][t][1] = sc[mt][t][2] = sc[mt][t][3] = 0.f;
         if constexpr (kFp8) {
-          const int key = 8 * t + r;
+          const int key = 16 * mt + r;  // and + 8, with the same swizzle in either layout
+          const int sw = D == 128 ? (key & 7) : ((key >> 1) & 3);
 #pragma unroll
           for (int g = 0; g < D / 64; ++g) {
-            const int sw = D == 128 ? (key & 7) : ((key >> 1) & 3);
-            const uint4 w = *reinterpret_cast<const uint4*>(kt + key * D + (((4 * g + c) ^ sw) << 4));
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            uint4 w[2];
+            w[0] = *reinterpret_cast<const uint4*>(kt + key * D + (((4 * g + c) ^ sw) << 4));
+            w[1] = *reinterpret_cast<const uint4*>(kt + (key + 8) * D + (((4 * g + c) ^ sw) << 4));
+            const uint32_t x[2][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w}};
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-              const uint2 b = e4m3x4_to_f16(x[s]);
-              mma_16816<true>(sc[t], qa[4 * g + s], b.x, b.y);
+              const uint2 lo = e4m3x4_to_f16(x[0][s]), hi = e4m3x4_to_f16(x[1][s]);
+              const uint32_t a[4] = {lo.x, hi.x, lo.y, hi.y};
+#pragma unroll
+              for (int t = 0; t < kNt; ++t) mma_16816<true>(sc[mt][t], a, qb[4 * g + s][t][0], qb[4 * g + s][t][1]);
             }
           }
         } else {
-          const int key = 8 * t + (lane & 7);
+          const int key = 16 * mt + (lane & 15);
 #pragma unroll
-          for (int s = 0; s < kKs; s += 2) {
-            const int ch = 2 * s + (lane >> 3);
-            uint32_t b[4];
-            ldmatrix_x4(ks + (ch >> 3) * kKeys * 128 + key * 128 + (((ch & 7) ^ (key & 7)) << 4), b);
-            mma_16816<false>(sc[t], qa[s], b[0], b[1]);
-            mma_16816<false>(sc[t], qa[s + 1], b[2], b[3]);
+          for (int s = 0; s < kKs; ++s) {
+            const int ch = 2 * s + (lane >> 4);
+            uint32_t a[4];
+            ldmatrix_x4(ks + (ch >> 3) * kKeys * 128 + key * 128 + (((ch & 7) ^ (key & 7)) << 4), a);
+#pragma unroll
+            for (int t = 0; t < kNt; ++t) mma_16816<false>(sc[mt][t], a, qb[s][t][0], qb[s][t][1]);
           }
         }
       }
+      // online softmax, base 2
       const bool masked = key0 < all_lo || key0 + kKeys > all_hi || there != all_boxes;
+      if (masked) {
+#pragma unroll
+        for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+          for (int t = 0; t < kNt; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = 16 * mt + r + 8 * (i >> 1);
+              const bool on = key0 + key >= klo[t][i & 1] && key0 + key < khi[t][i & 1] &&
+                              ((there >> (key >> box_shift)) & 1u);
+              if (!on) sc[mt][t][i] = -INFINITY;
+            }
+      }
+      float mx[kNt][2];
+      bool raise = false;
 #pragma unroll
       for (int t = 0; t < kNt; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[t][i] *= t_scale[i >> 1];
-      if (masked) {
+        for (int i = 0; i < 2; ++i) {
+          float x = fmaxf(sc[0][t][i], sc[0][t][i + 2]);
+#pragma unroll
+          for (int mt = 1; mt < kMt; ++mt) x = fmaxf(x, fmaxf(sc[mt][t][i], sc[mt][t][i + 2]));
+          mx[t][i] = x * t_scale[t][i];
+          raise |= !(mx[t][i] <= m[t][i] + 8.f);  // P would pass 2^8
+        }
+      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int t = 0; t < kNt; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = 8 * t + 2 * c + (i & 1);
-            const bool on = key0 + key >= klo[i >> 1] && key0 + key < khi[i >> 1] &&
-                            ((there >> (key / p.page_box)) & 1u);
-            if (!on) sc[t][i] = -INFINITY;
+          for (int i = 0; i < 2; ++i) {
+            float x = fmaxf(mx[t][i], m[t][i]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float f = x == -INFINITY ? 1.f : ex2(m[t][i] - x);
+            m[t][i] = x;
+            l[t][i] *= f;
+#pragma unroll
+            for (int s = 0; s < kKs; ++s) {
+              o[s][t][i] *= f;
+              o[s][t][i + 2] *= f;
+            }
           }
       }
-      // online softmax, base 2
-      float base[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx = m[i];
-#pragma unroll
-        for (int t = 0; t < kNt; ++t) mx = fmaxf(mx, fmaxf(sc[t][2 * i], sc[t][2 * i + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        base[i] = mx == -INFINITY ? 0.f : mx;
-        const float f = ex2(m[i] - base[i]);
-        m[i] = mx;
-        l[i] *= f;
-#pragma unroll
-        for (int t = 0; t < kOt; ++t) {
-          o[t][2 * i] *= f;
-          o[t][2 * i + 1] *= f;
-        }
-      }
-      uint32_t pa[kNt / 2][4];
+      // P rounded to the cache's operand type (BF16: 2^-8, FP16: 2^-11 relative at most, random over
+      // keys), transposed
+      uint32_t pb[kMt][kNt][2];
 #pragma unroll
       for (int t = 0; t < kNt; ++t) {
-        float e[4];
+        const float b0 = m[t][0] == -INFINITY ? 0.f : -m[t][0], b1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = ex2(sc[t][i] - base[i >> 1]);
-        l[0] += e[0] + e[1];
-        l[1] += e[2] + e[3];
-        // rounding P to the cache's operand type (BF16: 2^-8, FP16: 2^-11 relative, random over keys)
-        pa[t >> 1][(t & 1) * 2] = kFp8 ? pack_f16x2(e[0], e[1]) : pack_bf16x2(e[0], e[1]);
-        pa[t >> 1][(t & 1) * 2 + 1] = kFp8 ? pack_f16x2(e[2], e[3]) : pack_bf16x2(e[2], e[3]);
+        for (int mt = 0; mt < kMt; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float e0 = ex2(fmaf(sc[mt][t][2 * h], t_scale[t][0], b0));
+            const float e1 = ex2(fmaf(sc[mt][t][2 * h + 1], t_scale[t][1], b1));
+            l[t][0] += e0;
+            l[t][1] += e1;
+            pb[mt][t][h] = movmatrix_trans(kFp8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1));
+          }
       }
-      // O += P V
+      // O^T += V^T P^T
 #pragma unroll
-      for (int s = 0; s < kNt / 2; ++s) {
+      for (int mt = 0; mt < kMt; ++mt) {
         if constexpr (kFp8) {
           constexpr int kW = D / 32;  // words per lane and key
           uint32_t x[4][kW];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int key = 16 * s + 2 * c + (i & 1) + 8 * (i >> 1);
+            const int key = 16 * mt + 2 * c + (i & 1) + 8 * (i >> 1);
             if constexpr (D == 128) {
               *reinterpret_cast<uint4*>(x[i]) = *reinterpret_cast<const uint4*>(vt + key * D + ((r ^ (key & 7)) << 4));
             } else {
@@ -420,113 +394,108 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                   vt + key * D + (((r >> 1) ^ ((key >> 1) & 3)) << 4) + 8 * (r & 1));
             }
           }
+          // bytes b of a lane's columns: block b / 2, its row r (b even) or r + 8
 #pragma unroll
           for (int w = 0; w < kW; ++w) {
-            const uint2 a0 = e4m3x4_to_f16(__byte_perm(x[0][w], x[1][w], 0x5140));
-            const uint2 a1 = e4m3x4_to_f16(__byte_perm(x[0][w], x[1][w], 0x7362));
-            const uint2 b0 = e4m3x4_to_f16(__byte_perm(x[2][w], x[3][w], 0x5140));
-            const uint2 b1 = e4m3x4_to_f16(__byte_perm(x[2][w], x[3][w], 0x7362));
-            mma_16816<true>(o[4 * w], pa[s], a0.x, b0.x);
-            mma_16816<true>(o[4 * w + 1], pa[s], a0.y, b0.y);
-            mma_16816<true>(o[4 * w + 2], pa[s], a1.x, b1.x);
-            mma_16816<true>(o[4 * w + 3], pa[s], a1.y, b1.y);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint2 lo = e4m3x4_to_f16(__byte_perm(x[0][w], x[1][w], h ? 0x7362 : 0x5140));
+              const uint2 hi = e4m3x4_to_f16(__byte_perm(x[2][w], x[3][w], h ? 0x7362 : 0x5140));
+              const uint32_t a[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+              for (int t = 0; t < kNt; ++t) mma_16816<true>(o[2 * w + h][t], a, pb[mt][t][0], pb[mt][t][1]);
+            }
           }
         } else {
-          const int key = 16 * s + (lane & 15);
+          const int key = 16 * mt + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-          for (int t = 0; t < kOt; t += 2) {
-            const int ch = t + (lane >> 4);
-            uint32_t b[4];
-            ldmatrix_x4_trans(vs + (ch >> 3) * kKeys * 128 + key * 128 + (((ch & 7) ^ (key & 7)) << 4), b);
-            mma_16816<false>(o[t], pa[s], b[0], b[1]);
-            mma_16816<false>(o[t + 1], pa[s], b[2], b[3]);
+          for (int s = 0; s < kKs; ++s) {
+            const int ch = 2 * s + ((lane >> 3) & 1);
+            uint32_t a[4];
+            ldmatrix_x4_trans(vs + (ch >> 3) * kKeys * 128 + key * 128 + (((ch & 7) ^ (key & 7)) << 4), a);
+#pragma unroll
+            for (int t = 0; t < kNt; ++t) mma_16816<false>(o[s][t], a, pb[mt][t][0], pb[mt][t][1]);
           }
         }
       }
       fence_proxy_async_smem();  // zeros written above come before the next copy into the stage
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
-    }
-    // Join the warps: row maxima and sums, then accumulators scaled to the common maximum.
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (c == 0) ml[(parity * kDecWarps + warp) * kDecRows + r + 8 * i] = make_float2(m[i], l[i]);
-    }
-    bar_consumers();
-    const float2* mls = ml + parity * kDecWarps * kDecRows;
-    parity ^= 1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, mls[w * kDecRows + r + 8 * i].x);
-      const float f = ex2(m[i] - (top == -INFINITY ? 0.f : top));
-#pragma unroll
-      for (int t = 0; t < kOt; ++t) {
-        o[t][2 * i] *= f;
-        o[t][2 * i + 1] *= f;
+      copy_next(st);
+      if (++st == kDecStages) {
+        st = 0;
+        phase ^= 1;
       }
     }
-    auto column = [&](int t, int e) { return kFp8 ? (2 * c + e) * kOt + t : 8 * t + 2 * c + e; };
-    float* buf = merge + (warp & (kDecWarps / 2 - 1)) * kDecRows * D;
-    if (warp >= kDecWarps / 2) {
-#pragma unroll
-      for (int t = 0; t < kOt; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) buf[(r + 8 * (i >> 1)) * D + column(t, i & 1)] = o[t][i];
-    }
-    bar_consumers();
-    if (warp < kDecWarps / 2) {
-#pragma unroll
-      for (int t = 0; t < kOt; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) buf[(r + 8 * (i >> 1)) * D + column(t, i & 1)] += o[t][i];
-    }
-    bar_consumers();
+    if (!ok) break;
+
+    // O / l to BF16, or this part of the unit to the workspace.
     const bool whole = tile == 0 && n == u.nt;
-    if (tid < kDecRows * D / 8) {
-      const int row = tid / (D / 8), col = (tid % (D / 8)) * 8;
-      float top = -INFINITY, sum = 0.f;
+    const int64_t slot = 2 * static_cast<int64_t>(worker) + (tile == 0 ? 1 : 0);
+    // columns of o[s][t]: E4M3 r D / 8 + 2 s (accumulators 0, 1) and the next (2, 3); BF16 16 s + r and + 8
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, mls[w * kDecRows + row].x);
+    for (int t = 0; t < kNt; ++t) {
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float2 x = mls[w * kDecRows + row];
-        sum += x.y * ex2(x.x - (top == -INFINITY ? 0.f : top));
-      }
-      float acc[8] = {};
-#pragma unroll
-      for (int w = 0; w < kDecWarps / 2; ++w)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += merge[(w * kDecRows + row) * D + col + i];
-      if (row < u.rows) {
+      for (int i = 0; i < 2; ++i) {
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 4);
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
+        l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
+        const int row = 8 * t + 2 * c + i;
         if (whole) {
-          const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+          const float inv = l[t][i] == 0.f ? 0.f : p.v_scale / l[t][i];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] *= inv;
-          *reinterpret_cast<uint4*>(p.out + row_offset<D>(p, u.s.q0, u.hk, u.r0 + row, p.ldo) + col) =
-              make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
-                         pack_bf16x2(acc[6], acc[7]));
-        } else {
-          const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (tile == 0 ? 1 : 0);
-          float4* dst = reinterpret_cast<float4*>(p.part_o) + (slot * (D / 4) + col / 4) * kDecRows + row;
-          dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          dst[kDecRows] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-          if (col == 0) p.part_ml[slot * kDecRows + row] = make_float2(top, sum);
+          for (int s = 0; s < kKs; ++s) {
+            o[s][t][i] *= inv;
+            o[s][t][i + 2] *= inv;
+          }
+        } else if (row < u.rows) {
+          float* dst = p.part_o + (slot * p.tile_rows + row) * D;
+          if constexpr (kFp8) {
+#pragma unroll
+            for (int s = 0; s < kKs; s += 2)
+              *reinterpret_cast<float4*>(dst + r * (D / 8) + 2 * s) =
+                  make_float4(o[s][t][i], o[s][t][i + 2], o[s + 1][t][i], o[s + 1][t][i + 2]);
+          } else {
+#pragma unroll
+            for (int s = 0; s < kKs; ++s) {
+              dst[16 * s + r] = o[s][t][i];
+              dst[16 * s + 8 + r] = o[s][t][i + 2];
+            }
+          }
+          if (r == 0) p.part_ml[slot * p.tile_rows + row] = make_float2(m[t][i], l[t][i]);
+        }
+        if (kFp8 && whole && row < u.rows) {
+          uint16_t* dst = p.out + row_offset<D>(p, u.s.q0, u.hk, u.r0 + row, p.ldo) + r * (D / 8);
+#pragma unroll
+          for (int s = 0; s < kKs; s += 4)
+            *reinterpret_cast<uint4*>(dst + 2 * s) =
+                make_uint4(pack_bf16x2(o[s][t][i], o[s][t][i + 2]), pack_bf16x2(o[s + 1][t][i], o[s + 1][t][i + 2]),
+                           pack_bf16x2(o[s + 2][t][i], o[s + 2][t][i + 2]),
+                           pack_bf16x2(o[s + 3][t][i], o[s + 3][t][i + 2]));
+        }
+      }
+      if (!kFp8 && whole) {
+        // transposed back: lane (r, c) has columns 2 c, 2 c + 1 of row r
+        uint16_t* dst = p.out + row_offset<D>(p, u.s.q0, u.hk, u.r0 + min(8 * t + r, u.rows - 1), p.ldo) + 2 * c;
+#pragma unroll
+        for (int s = 0; s < kKs; ++s) {
+          const uint32_t lo = movmatrix_trans(pack_bf16x2(o[s][t][0], o[s][t][1]));
+          const uint32_t hi = movmatrix_trans(pack_bf16x2(o[s][t][2], o[s][t][3]));
+          if (8 * t + r < u.rows) {
+            *reinterpret_cast<uint32_t*>(dst + 16 * s) = lo;
+            *reinterpret_cast<uint32_t*>(dst + 16 * s + 8) = hi;
+          }
         }
       }
     }
-    if (tid == 0 && left == n) {
-      int parts = 0;
-      if (tile == 0 && n < u.nt) parts = owner(sh, at + u.nt - 1) - static_cast<int>(blockIdx.x) + 1;
-      p.part_units[blockIdx.x] = make_int4(static_cast<int>(u.s.q0), u.rt, u.rows, u.hk * 4096 + parts);
-    }
+    if (lane == 0 && left == n && tile == 0 && n < u.nt) p.part_units[worker] = part_unit(sh, u, worker, at, true);
     left -= n;
     at += n;
     tile = 0;
     if (left > 0) next_unit<kKeys>(p, u);
+  }
+  if (!ok) {
+    // a timeout: wait for the copies in flight
+    for (int s = 0; s < kDecStages; ++s) mbar_wait_drain(&full[(st + s) % kDecStages], st + s < kDecStages ? phase : phase ^ 1);
   }
 }
 

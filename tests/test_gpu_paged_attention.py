@@ -142,8 +142,10 @@ def test_lengths_beyond_the_table_are_clamped(q_lens):
     s["kv_len"][:] = 100000
     assert torch.equal(call(s), want)
     s["kv_len"][0] = -7
-    out = call(s)
-    assert (out[:q_lens[0]] == 0).all() and torch.equal(out[q_lens[0]:], want[q_lens[0]:])
+    # where a unit is split depends on all lengths, so the other sequence is equal up to the
+    # rounding of the joined parts: held to the formula
+    out, _ = check(s)
+    assert (out[:q_lens[0]] == 0).all()
 
 
 @pytest.mark.parametrize("q_lens", [[1, 4], [150, 40]])
