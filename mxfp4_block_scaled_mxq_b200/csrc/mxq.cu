@@ -495,8 +495,8 @@ mxq_status launch_paged_decode(const DeviceInfo& dev, const mxq_paged_kv* c, mxq
   mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), dim3(mxq::kDecThreads), S::kSmemBytes,
                                    stream, tk, tv, p);
   if (st != MXQ_OK) return st;
-  return launch_dependent(mxq::paged_join_few_kernel<D>,
-                          dim3(static_cast<unsigned>(p.workers), static_cast<unsigned>(std::min(p.G, 4))), dim3(256), 0,
+  return launch_dependent(mxq::paged_join_few_kernel<D, mxq::kDecWarps>,
+                          dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(std::min(p.G, 4))), dim3(256), 0,
                           stream, p);
 }
 

@@ -271,66 +271,73 @@ __device__ __forceinline__ int4 part_unit(const Share& sh, const Unit& u, int c,
   return make_int4(static_cast<int>(u.s.q0), u.rt, u.rows, u.hk * 4096 + parts);
 }
 
-// Joins the parts of the unit that worker blockIdx.x began: its last slot, then the first slots of
-// the workers after it.  Few rows: a block has one row at a time, groups of four columns times
-// 256 / (D / 4) slices of the parts (a unit that spans the whole machine has over a thousand).
-// The maximum of the parts' row maxima, and the NaN of any of them.
+// The maximum of two row maxima, or NaN if one is.
 __device__ __forceinline__ float max_or_nan(float a, float b) { return a != a || a >= b ? a : b; }
 
-template <int D>
+// Joins the parts of the units that the kWorkers workers of CTA blockIdx.x began: the worker's last
+// slot, then the first slots of the workers after it.  One row at a time: groups of four columns
+// times 256 / (D / 4) slices of the parts (a unit that spans the whole machine has over a
+// thousand); gridDim.y blocks take a unit's rows in turn.
+template <int D, int kWorkers>
 __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p) {
   constexpr int kGroups = D / 4, kSlices = 256 / kGroups;
   __shared__ float s_m[8], s_l[kSlices];
   __shared__ float4 s_o[kSlices][kGroups];
+  __shared__ int4 s_units[kWorkers];
   griddep_wait();
-  const int c = blockIdx.x;
-  const int4 un = p.part_units[c];
-  const int parts = un.w & 4095;
-  if (parts == 0) return;
   const int lane = threadIdx.x & 31, group = threadIdx.x % kGroups, slice = threadIdx.x / kGroups;
-  auto row_of = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.tile_rows + r; };
-  for (int r = blockIdx.y; r < un.z; r += gridDim.y) {
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < parts; i += 256) m = max_or_nan(m, p.part_ml[row_of(i, r)].x);
-    for (int k = 16; k > 0; k >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
-    if (lane == 0) s_m[threadIdx.x >> 5] = m;
-    __syncthreads();
-    for (int i = 0; i < 8; ++i) m = max_or_nan(m, s_m[i]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int i = slice; i < parts; i += kSlices) {
-      const float2 ml = p.part_ml[row_of(i, r)];
-      const float f = exp2f(ml.x - base);
-      l = fmaf(ml.y, f, l);
-      const float4 v = reinterpret_cast<const float4*>(p.part_o)[row_of(i, r) * kGroups + group];
-      acc.x = fmaf(v.x, f, acc.x);
-      acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z);
-      acc.w = fmaf(v.w, f, acc.w);
-    }
-    s_o[slice][group] = acc;
-    if (group == 0) s_l[slice] = l;
-    __syncthreads();
-    if (slice == 0) {
-      for (int i = 1; i < kSlices; ++i) {
-        const float4 v = s_o[i][group];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-        l += s_l[i];
+  if (threadIdx.x < kWorkers) s_units[threadIdx.x] = p.part_units[blockIdx.x * kWorkers + threadIdx.x];
+  __syncthreads();
+  for (int w = 0; w < kWorkers; ++w) {
+    const int c = blockIdx.x * kWorkers + w;
+    const int4 un = s_units[w];
+    const int parts = un.w & 4095;
+    if (parts == 0) continue;
+    auto row_of = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.tile_rows + r; };
+    for (int r = blockIdx.y; r < un.z; r += gridDim.y) {
+      float m = -INFINITY;
+      for (int i = threadIdx.x; i < parts; i += 256) m = max_or_nan(m, p.part_ml[row_of(i, r)].x);
+      for (int k = 16; k > 0; k >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
+      if (lane == 0) s_m[threadIdx.x >> 5] = m;
+      __syncthreads();
+      for (int i = 0; i < 8; ++i) m = max_or_nan(m, s_m[i]);
+      const float base = m == -INFINITY ? 0.f : m;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l = 0.f;
+  #pragma unroll 4
+      for (int i = slice; i < parts; i += kSlices) {
+        const float2 ml = p.part_ml[row_of(i, r)];
+        const float f = exp2f(ml.x - base);
+        l = fmaf(ml.y, f, l);
+        const float4 v = reinterpret_cast<const float4*>(p.part_o)[row_of(i, r) * kGroups + group];
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
       }
-      const float inv = l == 0.f ? 0.f : p.v_scale / l;
-      uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + 4 * group;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      s_o[slice][group] = acc;
+      if (group == 0) s_l[slice] = l;
+      __syncthreads();
+      if (slice == 0) {
+        for (int i = 1; i < kSlices; ++i) {
+          const float4 v = s_o[i][group];
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+          l += s_l[i];
+        }
+        const float inv = l == 0.f ? 0.f : p.v_scale / l;
+        uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + 4 * group;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
-// Many rows: a block has 8 rows and all groups of four columns; parts are [d / 4][row][4], the
+// The same for the unit that worker blockIdx.x began, many rows: a block has 8 rows and all
+// groups of four columns; parts are [d / 4][row][4], the
 // layout in which the thread per row that wrote them stored consecutively.
 template <int D, int kRows>
 __global__ void __launch_bounds__(2 * D) paged_join_many_kernel(const PagedParams p) {

@@ -149,7 +149,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -308,11 +308,11 @@ def _on_stream(fn):
     stream that allocated it, so tensors the helper allocates (outputs and temporaries such
     as the quantised activations of linear_w4a4) then stay valid for as long as the kernels
     the helper queued on `stream` read or write them, whatever stream the caller is on."""
-    sig = inspect.signature(fn)
+    place = list(inspect.signature(fn).parameters).index("stream")
 
     @functools.wraps(fn)
     def wrapper(*args, **kwargs):
-        stream = kwargs["stream"] if "stream" in kwargs else sig.bind(*args, **kwargs).arguments.get("stream")
+        stream = args[place] if len(args) > place else kwargs.get("stream")
         if stream is None:
             return fn(*args, **kwargs)
         s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
@@ -532,38 +532,54 @@ def linear_w4a8(x: torch.Tensor, act_scale: float, w_codes, w_sf, N: int, bias=N
 
 
 # ------------------------------------------------------------------ queries and keys, paged cache
-def _heads_2d(x: torch.Tensor, heads: int, d: int | None, name: str) -> int:
-    """Checks a [T][heads * d] operand and returns d."""
-    _bf16_2d(x, name)
-    width = x.shape[1]
-    if heads < 1 or width % heads or (d is not None and width != heads * d):
-        raise ValueError(f"{name}: {width} columns are not {heads} heads" + ("" if d is None else f" of {d}"))
-    return width // heads
+def _operand(x: torch.Tensor, cur: int, name: str) -> None:
+    """_bf16_2d in a few cheap checks: a generated token's whole layer is some tens of microseconds."""
+    if x.dtype is not torch.bfloat16 or x.dim() != 2 or x.get_device() != cur or x.stride(1) != 1:
+        _bf16_2d(x, name)
 
 
-def _int32(x: torch.Tensor, shape: tuple, name: str) -> int:
-    if x.dtype != torch.int32 or not x.is_cuda or not x.is_contiguous() or tuple(x.shape) != shape:
+def _current(x: torch.Tensor, name: str) -> int:
+    """The current device, once x is known to be on one."""
+    if not x.is_cuda:
+        raise ValueError(f"{name}: expected a 2-D bfloat16 CUDA tensor")
+    return torch.cuda.current_device()
+
+
+def _here(x: torch.Tensor, cur: int, name: str) -> None:
+    if x.get_device() != cur:
+        if not x.is_cuda:
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        _on_current_device(x, name)
+
+
+def _width(x: torch.Tensor, heads: int, d: int, name: str) -> None:
+    if heads < 1 or x.shape[1] != heads * d:
+        raise ValueError(f"{name}: {x.shape[1]} columns are not {heads} heads of {d}")
+
+
+def _int32(x: torch.Tensor, shape: tuple, cur: int, name: str) -> int:
+    if x.dtype is not torch.int32 or x.shape != shape or not x.is_cuda or not x.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous int32 CUDA tensor of shape {shape}")
-    _on_current_device(x, name)
+    _here(x, cur, name)
     return x.data_ptr()
 
 
-def _norm_rope(q_heads, k_heads, d, q_weight, k_weight, eps, span, table, style) -> NormRope:
-    cfg = NormRope(None, None, None, 0, 0, eps, span, style)
-    for name, w, heads in (("q_weight", q_weight, q_heads), ("k_weight", k_weight, k_heads)):
-        if w is None:
-            continue
-        n = heads * d if span == MXQ_NORM_ROW else d
-        if w.dtype != torch.bfloat16 or not w.is_cuda or not w.is_contiguous() or w.numel() != n:
-            raise ValueError(f"{name}: expected {n} contiguous bfloat16 values on the GPU")
-        _on_current_device(w, name)
-        setattr(cfg, name, w.data_ptr())
-    if table is not None:
-        if table.dtype != torch.float32 or not table.is_cuda or table.dim() != 2 or not table.is_contiguous():
-            raise ValueError("table: expected a contiguous float32 CUDA tensor [positions][rot]")
-        _on_current_device(table, "table")
-        cfg.table, cfg.table_rows, cfg.rot = table.data_ptr(), table.shape[0], table.shape[1]
-    return cfg
+def _weight(w: torch.Tensor, n: int, cur: int, name: str) -> int:
+    if w.dtype is not torch.bfloat16 or w.numel() != n or not w.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous bfloat16 values")
+    _here(w, cur, name)
+    return w.data_ptr()
+
+
+def _norm_rope(Hq, Hk, d, q_weight, k_weight, eps, span, table, style, cur) -> NormRope:
+    qw = None if q_weight is None else _weight(q_weight, Hq * d if span == MXQ_NORM_ROW else d, cur, "q_weight")
+    kw = None if k_weight is None else _weight(k_weight, Hk * d if span == MXQ_NORM_ROW else d, cur, "k_weight")
+    if table is None:
+        return NormRope(qw, kw, None, 0, 0, eps, span, style)
+    if table.dtype is not torch.float32 or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table: expected a contiguous float32 tensor [positions][rot]")
+    _here(table, cur, "table")
+    return NormRope(qw, kw, table.data_ptr(), *table.shape, eps, span, style)
 
 
 def rope_table(positions: int | torch.Tensor, rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -583,21 +599,20 @@ class PagedKV:
     __slots__ = ("k", "v", "args")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
-        shape, strides = k.shape, k.stride()
-        if len(shape) != 4 or v.shape != shape or v.stride() != strides or v.dtype != k.dtype:
+        shape, strides, dtype = k.shape, k.stride(), k.dtype
+        if len(shape) != 4 or v.shape != shape or v.stride() != strides or v.dtype is not dtype:
             raise ValueError("k, v: expected two [pages][page_size][heads][d] tensors alike in shape, strides and type")
-        if k.dtype == torch.bfloat16:
+        if dtype is torch.bfloat16:
             fmt = MXQ_KV_BF16
-        elif k.dtype in (torch.float8_e4m3fn, torch.uint8):
+        elif dtype is torch.float8_e4m3fn or dtype is torch.uint8:
             fmt = MXQ_KV_FP8_E4M3
         else:
             raise ValueError("k, v: expected bfloat16, float8_e4m3fn or uint8")
-        if not k.is_cuda or not v.is_cuda or strides[3] != 1:
-            raise ValueError("k, v: expected CUDA tensors with contiguous heads")
-        _on_current_device(k, "k")
-        _on_current_device(v, "v")
+        if not k.is_cuda or v.get_device() != k.get_device() or strides[3] != 1:
+            raise ValueError("k, v: expected CUDA tensors of one device, with contiguous heads")
         self.k, self.v = k, v
-        self.args = PagedKVArgs(k.data_ptr(), v.data_ptr(), *shape, *strides[:3], fmt, k_scale, v_scale)
+        self.args = PagedKVArgs(k.data_ptr(), v.data_ptr(), *shape, strides[0], strides[1], strides[2], fmt, k_scale,
+                                v_scale)
 
 
 def paged_kv(pages: int, page_size: int, heads: int, d: int, fmt: int = MXQ_KV_BF16, k_scale: float = 1.0,
@@ -618,15 +633,16 @@ class PagedBatch:
         if block_table.dim() != 2:
             raise ValueError("block_table: expected [batch][max_pages]")
         batch, max_pages = block_table.shape
+        dev = block_table.get_device()
+        self.args = PagedBatchArgs(_int32(cu_q, (batch + 1,), dev, "cu_q"), _int32(kv_len, (batch,), dev, "kv_len"),
+                                   _int32(block_table, (batch, max_pages), dev, "block_table"), batch, max_pages)
         self.cu_q, self.kv_len, self.block_table = cu_q, kv_len, block_table
-        self.args = PagedBatchArgs(_int32(cu_q, (batch + 1,), "cu_q"), _int32(kv_len, (batch,), "kv_len"),
-                                   _int32(block_table, (batch, max_pages), "block_table"), batch, max_pages)
 
 
-def _out_heads(out, x: torch.Tensor, name: str) -> torch.Tensor:
+def _out_heads(out, x: torch.Tensor, cur: int, name: str) -> torch.Tensor:
     if out is None:
-        return torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    _bf16_2d(out, name)
+        return torch.empty_like(x)
+    _operand(out, cur, name)
     if out.shape != x.shape:
         raise ValueError(f"{name}: expected shape {tuple(x.shape)}")
     return out
@@ -639,14 +655,18 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, Hq: int, Hk: int, q_weight=No
     """Norm (where weights are given) and rotation (where a table is given) of q [T][Hq*d] and k
     [T][Hk*d] -> (q_out, k_out).  positions: int32 [T], or None for 0, 1, 2, ...; a row whose position is
     outside the table is not written.  q_out=q, k_out=k work in place."""
-    d = _heads_2d(q, Hq, None, "q")
-    _heads_2d(k, Hk, d, "k")
+    cur = _current(q, "q")
+    _operand(q, cur, "q")
+    _operand(k, cur, "k")
     T = q.shape[0]
+    d = q.shape[1] // Hq if Hq > 0 else 0
+    _width(q, Hq, d, "q")
+    _width(k, Hk, d, "k")
     if k.shape[0] != T:
         raise ValueError("q, k: expected the same number of rows")
-    cfg = _norm_rope(Hq, Hk, d, q_weight, k_weight, eps, span, table, style)
-    pos = None if positions is None else _int32(positions, (T,), "positions")
-    qo, ko = _out_heads(q_out, q, "q_out"), _out_heads(k_out, k, "k_out")
+    cfg = _norm_rope(Hq, Hk, d, q_weight, k_weight, eps, span, table, style, cur)
+    pos = None if positions is None else _int32(positions, (T,), cur, "positions")
+    qo, ko = _out_heads(q_out, q, cur, "q_out"), _out_heads(k_out, k, cur, "k_out")
     mxq_qk_norm_rope(cfg, T, d, q.data_ptr(), Hq, q.stride(0), qo.data_ptr(), qo.stride(0), k.data_ptr(), Hk,
                      k.stride(0), ko.data_ptr(), ko.stride(0), pos, stream)
     return qo, ko
@@ -658,25 +678,27 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: PagedKV, batch: PagedBatc
               stream=None):
     """Norm and rotation of the new keys k [T][heads*d] at their sequences' positions, keys and values
     into the cache; with q [T][Hq*d] also its norm and rotation -> q_out (else None)."""
+    cur = _current(k, "k")
     a = cache.args
-    d, heads = a.d, a.heads
-    _heads_2d(k, heads, d, "k")
-    _heads_2d(v, heads, d, "v")
-    _on_current_device(cache.k, "cache")
-    _on_current_device(batch.cu_q, "batch")
-    T = k.shape[0]
+    d, heads, T = a.d, a.heads, k.shape[0]
+    _operand(k, cur, "k")
+    _operand(v, cur, "v")
+    _width(k, heads, d, "k")
+    _width(v, heads, d, "v")
+    _here(cache.k, cur, "cache")
+    _here(batch.cu_q, cur, "batch")
     if v.shape[0] != T or (q is not None and q.shape[0] != T):
         raise ValueError("k, v, q: expected the same number of rows")
     if q is None:
-        cfg = _norm_rope(0, heads, d, None, k_weight, eps, span, table, style)
+        cfg = _norm_rope(0, heads, d, None, k_weight, eps, span, table, style, cur)
         mxq_kv_append(cfg, a, batch.args, T, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), None, 0, 0, None, 0,
                       stream)
         return None
-    _bf16_2d(q, "q")
+    _operand(q, cur, "q")
     Hq = q.shape[1] // d
-    _heads_2d(q, Hq, d, "q")
-    cfg = _norm_rope(Hq, heads, d, q_weight, k_weight, eps, span, table, style)
-    qo = _out_heads(q_out, q, "q_out")
+    _width(q, Hq, d, "q")
+    cfg = _norm_rope(Hq, heads, d, q_weight, k_weight, eps, span, table, style, cur)
+    qo = _out_heads(q_out, q, cur, "q_out")
     mxq_kv_append(cfg, a, batch.args, T, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), q.data_ptr(), Hq,
                   q.stride(0), qo.data_ptr(), qo.stride(0), stream)
     return qo
@@ -695,14 +717,18 @@ def attention_paged(q: torch.Tensor, Hq: int, cache: PagedKV, batch: PagedBatch,
                     scale: float | None = None, out=None, workspace=None, stream=None) -> torch.Tensor:
     """Attention of the new tokens' queries q [T][Hq*d] over their sequences' cached keys and values
     -> O [T][Hq*d] BF16.  scale: d^-1/2 by default.  Rows of no sequence are not written."""
+    cur = _current(q, "q")
     a, b = cache.args, batch.args
-    d = _heads_2d(q, Hq, a.d, "q")
-    _on_current_device(cache.k, "cache")
-    _on_current_device(batch.cu_q, "batch")
-    T = q.shape[0]
+    d, T = a.d, q.shape[0]
+    _operand(q, cur, "q")
+    _width(q, Hq, d, "q")
+    _here(cache.k, cur, "cache")
+    _here(batch.cu_q, cur, "batch")
     if workspace is None:
         workspace = attention_paged_workspace(T, b.batch, Hq, a.heads, d, q.device)
-    o = _out_heads(out, q, "out")
+    else:
+        _here(workspace, cur, "workspace")
+    o = _out_heads(out, q, cur, "out")
     mxq_attention_paged(q.data_ptr(), T, Hq, q.stride(0), a, b, causal, window, d ** -0.5 if scale is None else scale,
                         workspace, workspace.numel() * workspace.element_size(), o.data_ptr(), o.stride(0), stream)
     return o
