@@ -429,7 +429,8 @@ mxq_status launch_rope_cache(const mxq::RopeParams& p, const mxq::AppendParams& 
 }
 
 // 5-D tensor map over a paged cache: (128-byte piece of a head, token, piece, head, page).
-bool make_tmap_cache(CUtensorMap* m, const mxq_paged_kv* c, const void* base, int box_tokens) {
+// A box: box_tokens tokens of one head of one page, one piece or (whole) all.
+bool make_tmap_cache(CUtensorMap* m, const mxq_paged_kv* c, const void* base, int box_tokens, bool whole) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   const bool fp8 = c->fmt == MXQ_KV_FP8_E4M3;
@@ -438,7 +439,8 @@ bool make_tmap_cache(CUtensorMap* m, const mxq_paged_kv* c, const void* base, in
   const cuuint64_t dims[5] = {piece / size, static_cast<cuuint64_t>(c->page_size), row / piece,
                               static_cast<cuuint64_t>(c->heads), static_cast<cuuint64_t>(c->num_pages)};
   const cuuint64_t strides[4] = {c->stride_token * size, piece, c->stride_head * size, c->stride_page * size};
-  const cuuint32_t box[5] = {static_cast<cuuint32_t>(piece / size), static_cast<cuuint32_t>(box_tokens), 1, 1, 1};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(piece / size), static_cast<cuuint32_t>(box_tokens),
+                             whole ? static_cast<cuuint32_t>(row / piece) : 1, 1, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base),
             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -491,7 +493,8 @@ mxq_status launch_paged_decode(const DeviceInfo& dev, const mxq_paged_kv* c, mxq
   p.workers = ctas * mxq::kDecWarps;
   p.page_box = gcd(p.page_size, S::kKeys);
   CUtensorMap tk, tv;
-  if (!make_tmap_cache(&tk, c, c->k, p.page_box) || !make_tmap_cache(&tv, c, c->v, p.page_box)) return MXQ_ERR_CUDA;
+  if (!make_tmap_cache(&tk, c, c->k, p.page_box, true) || !make_tmap_cache(&tv, c, c->v, p.page_box, true))
+    return MXQ_ERR_CUDA;
   mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), dim3(mxq::kDecThreads), S::kSmemBytes,
                                    stream, tk, tv, p);
   if (st != MXQ_OK) return st;
@@ -540,8 +543,8 @@ mxq_status launch_paged_chunk(const DeviceInfo& dev, const mxq_paged_kv* c, mxq:
   p.tile_rows = 2 * tokens * p.G;
   p.page_box = gcd(p.page_size, kFp8 ? S::kRawKeys : mxq::kChunkKeys);
   CUtensorMap tq, tk, tv;
-  if (!make_tmap_q(&tq, p, D, tokens) || !make_tmap_cache(&tk, c, c->k, p.page_box) ||
-      !make_tmap_cache(&tv, c, c->v, p.page_box))
+  if (!make_tmap_q(&tq, p, D, tokens) || !make_tmap_cache(&tk, c, c->k, p.page_box, false) ||
+      !make_tmap_cache(&tv, c, c->v, p.page_box, false))
     return MXQ_ERR_CUDA;
   mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(p.workers)), dim3(S::kThreads), S::kSmemBytes,
                                    stream, tq, tk, tv, p);

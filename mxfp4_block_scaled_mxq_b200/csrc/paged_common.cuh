@@ -137,6 +137,7 @@ constexpr int kMaxWorkers = 16;  // of one CTA
 
 struct ShareScratch {
   int64_t warp_sum[32];
+  int64_t bound[kMaxWorkers + 1];
   int64_t weight[kMaxWorkers], rest[kMaxWorkers];
   int b[kMaxWorkers];
 };
@@ -182,8 +183,11 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
     for (int i = 0; i < kWarps; ++i) total += sc.warp_sum[i];
   }
   const int64_t shares = min(static_cast<int64_t>(p.workers), (total + kMinTiles - 1) / kMinTiles);
-  auto bound = [&](int64_t c) { return c < shares ? total * c / shares : total; };
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kWorkers;
+  if (tid <= kWorkers) {  // the borders of this CTA's shares
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kWorkers + tid;
+    sc.bound[tid] = c < shares ? total * c / shares : total;
+  }
+  __syncthreads();
   int64_t before = 0;
   for (int r = 0; r < rounds; ++r) {
     const int b = r * per_round + (by_warp ? warp : tid);
@@ -201,11 +205,9 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
     int64_t lo = before + incl - mine;
     for (int i = 0; i < warp; ++i) lo += sc.warp_sum[i];
     if (mine > 0) {
-      // the first worker of this CTA whose share begins at or after lo: shares are in order
       for (int w = 0; w < kWorkers; ++w) {
-        const int64_t begin = bound(c0 + w);
-        if (begin >= lo + mine) break;
-        if (begin >= lo) {
+        const int64_t begin = sc.bound[w];
+        if (begin >= lo && begin < lo + mine) {
           sc.b[w] = b;
           sc.rest[w] = begin - lo;
           sc.weight[w] = mine;
@@ -217,8 +219,8 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
   __syncthreads();
   const int worker = kWorkers == 1 ? 0 : min(warp, kWorkers - 1);
   Share sh;
-  sh.begin = bound(c0 + worker);
-  sh.count = sc.b[worker] < 0 ? 0 : bound(c0 + worker + 1) - sh.begin;
+  sh.begin = sc.bound[worker];
+  sh.count = sc.b[worker] < 0 ? 0 : sc.bound[worker + 1] - sh.begin;
   sh.total = total;
   sh.shares = static_cast<int>(shares);
   sh.tile = 0;
@@ -275,9 +277,10 @@ __device__ __forceinline__ int4 part_unit(const Share& sh, const Unit& u, int c,
 __device__ __forceinline__ float max_or_nan(float a, float b) { return a != a || a >= b ? a : b; }
 
 // Joins the parts of the units that the kWorkers workers of CTA blockIdx.x began: the worker's last
-// slot, then the first slots of the workers after it.  One row at a time: groups of four columns
-// times 256 / (D / 4) slices of the parts (a unit that spans the whole machine has over a
-// thousand); gridDim.y blocks take a unit's rows in turn.
+// slot, then the first slots of the workers after it; gridDim.y blocks take a unit's rows in turn.
+// (A unit that spans the whole machine has over a thousand parts.)
+constexpr int kJoinWarpParts = 32;
+
 template <int D, int kWorkers>
 __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p) {
   constexpr int kGroups = D / 4, kSlices = 256 / kGroups;
@@ -288,11 +291,47 @@ __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p
   const int lane = threadIdx.x & 31, group = threadIdx.x % kGroups, slice = threadIdx.x / kGroups;
   if (threadIdx.x < kWorkers) s_units[threadIdx.x] = p.part_units[blockIdx.x * kWorkers + threadIdx.x];
   __syncthreads();
+  // Units of few parts: a warp each, D / 32 columns a lane.
+  static_assert(kWorkers == 8, "a warp per worker");
+  {
+    constexpr int kCols = D / 32;
+    const int w = threadIdx.x >> 5, c = blockIdx.x * kWorkers + w;
+    const int4 un = s_units[w];
+    const int parts = un.w & 4095;
+    for (int r = blockIdx.y; parts > 0 && parts <= kJoinWarpParts && r < un.z; r += gridDim.y) {
+      auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.tile_rows + r; };
+      const float2 mine = lane < parts ? p.part_ml[row_of(lane)] : make_float2(-INFINITY, 0.f);
+      float m = mine.x;
+      for (int k = 16; k > 0; k >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
+      const float f = exp2f(mine.x - (m == -INFINITY ? 0.f : m));
+      float l = mine.y * f;
+      for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+      float acc[kCols] = {};
+#pragma unroll 8
+      for (int i = 0; i < parts; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float* o = p.part_o + row_of(i) * D + lane * kCols;
+        float v[kCols];
+        if constexpr (kCols == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
+        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) acc[k] = fmaf(v[k], fi, acc[k]);
+      }
+      const float inv = l == 0.f ? 0.f : p.v_scale / l;
+      uint32_t h[kCols / 2];
+#pragma unroll
+      for (int k = 0; k < kCols / 2; ++k) h[k] = pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+      uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + lane * kCols;
+      if constexpr (kCols == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
+      else *reinterpret_cast<uint32_t*>(dst) = h[0];
+    }
+  }
+  // The others: the whole block, slices of the parts side by side.
   for (int w = 0; w < kWorkers; ++w) {
     const int c = blockIdx.x * kWorkers + w;
     const int4 un = s_units[w];
     const int parts = un.w & 4095;
-    if (parts == 0) continue;
+    if (parts <= kJoinWarpParts) continue;
     auto row_of = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.tile_rows + r; };
     for (int r = blockIdx.y; r < un.z; r += gridDim.y) {
       float m = -INFINITY;

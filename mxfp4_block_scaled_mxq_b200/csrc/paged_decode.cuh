@@ -43,7 +43,7 @@ struct DecShape {
   static constexpr int kBoxRowBytes = kRowBytes > 128 ? 128 : kRowBytes;  // one TMA box's row
   static constexpr int kHalves = kRowBytes / kBoxRowBytes;
   static constexpr int kSmemBytes = 1024 + kDecWarps * kDecStages * kDecStageBytes;
-  static_assert(kKeys >= 16 && kKeys / 8 * kHalves * 2 <= 32, "a lane for each copy");
+  static_assert(kKeys >= 16 && kKeys / 8 * 2 <= 32, "a lane for each copy");
 };
 
 __device__ __forceinline__ void tma_load_5d(void* smem_dst, const CUtensorMap* m, int32_t c0, int32_t c1, int32_t c2,
@@ -141,11 +141,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   uint8_t* ring = smem + warp * kDecStages * kDecStageBytes;
   uint64_t* full = full_bars[warp];
 
-  // Copies run kDecStages tiles ahead of the tile at hand.  Lane i has copy i of a tile: K or V, the
-  // 128-byte piece, the box.
+  // Copies run kDecStages tiles ahead of the tile at hand.  Lane i has copy i of a tile: a box of K,
+  // or of V.  The SM's copy engine takes some 20 ns a copy, so a box holds all of a token's bytes:
+  // its 128-byte pieces follow one another, each of page_box rows.
   const int nbox = kKeys / p.page_box, box_shift = 31 - __clz(p.page_box);
-  const int box = lane % nbox, piece = lane / nbox % S::kHalves;
-  const bool is_v = lane >= nbox * S::kHalves, copies = lane < nbox * S::kHalves * 2;
+  const int box = lane & (nbox - 1);
+  const bool is_v = lane >= nbox, copies = lane < nbox * 2;
+  const int piece_stride = p.page_box * 128;
+  auto key_offset = [&](int key) {  // of its first piece, in a tile
+    return (key >> box_shift) * p.page_box * S::kRowBytes + (key & (p.page_box - 1)) * S::kBoxRowBytes;
+  };
   Unit lu = sh.u;
   int ltile = sh.tile;
   int64_t lleft = sh.count;
@@ -170,9 +175,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (lane == 0) mbar_arrive_expect_tx(&full[stage], kDecStageBytes);
     __syncwarp();
     if (copies) {
-      uint8_t* dst = ring + stage * kDecStageBytes + (is_v ? S::kTileBytes : 0) + piece * kKeys * 128 +
-                     box * p.page_box * S::kBoxRowBytes;
-      tma_load_5d(dst, is_v ? &tmap_v : &tmap_k, 0, there ? box_key - entry * p.page_size : 0, piece, lu.hk,
+      uint8_t* dst = ring + stage * kDecStageBytes + (is_v ? S::kTileBytes : 0) + box * p.page_box * S::kRowBytes;
+      tma_load_5d(dst, is_v ? &tmap_v : &tmap_k, 0, there ? box_key - entry * p.page_size : 0, 0, lu.hk,
                   there ? page : -1, &full[stage]);  // page out of range: the box is filled with zeros
     }
     --lleft;
@@ -189,6 +193,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   // Fragments: lane (r, c) has row r (of eight) of a block as an operand, and rows 2 c, 2 c + 1 in
   // accumulators.
   const int r = lane >> 2, c = lane & 3;
+  int k_off[kMt], v_off[kMt];  // of this lane's rows for ldmatrix, BF16 (row & 7 = lane & 7 in both)
+#pragma unroll
+  for (int mt = 0; mt < kMt; ++mt) {
+    k_off[mt] = key_offset(16 * mt + (lane & 15));
+    v_off[mt] = key_offset(16 * mt + (lane & 7) + ((lane >> 4) << 3));
+  }
   Unit u = sh.u;
   int tile = sh.tile;
   int64_t left = sh.count, at = sh.begin;
@@ -274,7 +284,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           const int key = i / (S::kRowBytes / 16);
           if (key0 + key < u.lo || key0 + key >= u.hi) {
             const int ch = i % (S::kRowBytes / 16);
-            *reinterpret_cast<uint4*>(vt + (ch >> 3) * kKeys * 128 + key * S::kBoxRowBytes + (ch & 7) * 16) =
+            *reinterpret_cast<uint4*>(vt + key_offset(key) + (ch >> 3) * piece_stride + (ch & 7) * 16) =
                 make_uint4(0, 0, 0, 0);
           }
         }
@@ -304,12 +314,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
           }
         } else {
-          const int key = 16 * mt + (lane & 15);
 #pragma unroll
           for (int s = 0; s < kKs; ++s) {
             const int ch = 2 * s + (lane >> 4);
             uint32_t a[4];
-            ldmatrix_x4(ks + (ch >> 3) * kKeys * 128 + key * 128 + (((ch & 7) ^ (key & 7)) << 4), a);
+            ldmatrix_x4(ks + k_off[mt] + (ch >> 3) * piece_stride + (((ch & 7) ^ (lane & 7)) << 4), a);
 #pragma unroll
             for (int t = 0; t < kNt; ++t) mma_16816<false>(sc[mt][t], a, qb[s][t][0], qb[s][t][1]);
           }
@@ -407,12 +416,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
           }
         } else {
-          const int key = 16 * mt + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
           for (int s = 0; s < kKs; ++s) {
             const int ch = 2 * s + ((lane >> 3) & 1);
             uint32_t a[4];
-            ldmatrix_x4_trans(vs + (ch >> 3) * kKeys * 128 + key * 128 + (((ch & 7) ^ (key & 7)) << 4), a);
+            ldmatrix_x4_trans(vs + v_off[mt] + (ch >> 3) * piece_stride + (((ch & 7) ^ (lane & 7)) << 4), a);
 #pragma unroll
             for (int t = 0; t < kNt; ++t) mma_16816<false>(o[s][t], a, pb[mt][t][0], pb[mt][t][1]);
           }
