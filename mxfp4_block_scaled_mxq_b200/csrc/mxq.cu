@@ -499,7 +499,7 @@ mxq_status launch_paged_decode(const DeviceInfo& dev, const mxq_paged_kv* c, mxq
                                    stream, tk, tv, p);
   if (st != MXQ_OK) return st;
   return launch_dependent(mxq::paged_join_few_kernel<D, mxq::kDecWarps>,
-                          dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(std::min(p.G, 4))), dim3(256), 0,
+                          dim3(static_cast<unsigned>(ctas), 8), dim3(256), 0,
                           stream, p);
 }
 

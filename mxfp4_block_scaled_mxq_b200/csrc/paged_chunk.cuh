@@ -154,7 +154,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
   }
   griddep_launch_dependents();
   griddep_wait();
-  const Share sh = find_share<kChunkKeys, S::kThreads, 1, kChunkMinTiles>(p, scratch);
+  const Share sh = find_share<kChunkKeys, S::kThreads, 1, kChunkMinTiles, false>(p, scratch);
   if (tid == 0 && sh.count == 0) p.part_units[blockIdx.x] = make_int4(0, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
         if (!ok) break;
         left -= n;
         tile = 0;
-        if (left > 0) next_unit<kChunkKeys>(p, u);
+        if (left > 0) next_unit<kChunkKeys, false>(p, u);
       }
       if (!ok) {
         if (units) mbar_wait_drain(q_full, (units - 1) & 1);
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           ++units;
           left -= n;
           tile = 0;
-          if (left > 0) next_unit<kChunkKeys>(p, u);
+          if (left > 0) next_unit<kChunkKeys, false>(p, u);
         }
         if (!ok) {
           tc_commit(drain);
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           }
           left -= n;
           tile = 0;
-          if (ok && left > 0) next_unit<kChunkKeys>(p, u);
+          if (ok && left > 0) next_unit<kChunkKeys, false>(p, u);
         }
       }
     }
@@ -669,13 +669,13 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
         }
       }
       if (tid == 0 && left == n)
-        p.part_units[blockIdx.x] = part_unit(sh, u, static_cast<int>(blockIdx.x), at, tile == 0 && n < u.nt);
+        p.part_units[blockIdx.x] = part_unit(sh, u, at, tile == 0 && n < u.nt);
       g += n;
       ++units;
       left -= n;
       at += n;
       tile = 0;
-      if (ok && left > 0) next_unit<kChunkKeys>(p, u);
+      if (ok && left > 0) next_unit<kChunkKeys, false>(p, u);
     }
   }
   tc_fence_before();

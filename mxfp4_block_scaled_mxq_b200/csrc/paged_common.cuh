@@ -14,6 +14,11 @@
 // to the workspace as an unnormalised FP32 accumulator with its row maxima and sums (two
 // slots per worker, so the workspace does not grow with the lengths), and the joining kernel
 // adds the parts of each unit in the order of the keys.
+//
+// kPerHead (the few-row kernel, which has over a thousand workers): the line is one key head's, and
+// workers g, g + 1, ... take the same share of heads g mod Hk, so that the heads of a token are
+// read side by side at the same time (E4M3, d = 128, [page][token][head][d]: 128-byte pieces of
+// 1 KB rows).  Else the line goes over all key heads.
 #pragma once
 
 #include "gemm_common.cuh"
@@ -106,14 +111,14 @@ __device__ __forceinline__ int unit_tiles(const PagedParams& p, const Sequence& 
 }
 
 // The next unit in the line (row tiles within key heads within sequences).
-template <int kKeys>
+template <int kKeys, bool kPerHead>
 __device__ __forceinline__ void next_unit(const PagedParams& p, Unit& u) {
   if (u.rt + 1 < row_tiles(p, u.s)) {
     ++u.rt;
   } else {
     u.rt = 0;
-    if (++u.hk == p.Hk) {
-      u.hk = 0;
+    if (kPerHead || ++u.hk == p.Hk) {
+      if (!kPerHead) u.hk = 0;
       do {
         ++u.b;
         if (u.b >= p.batch) return;  // only past the last share
@@ -130,16 +135,17 @@ struct Share {
   int tile;              // first key tile within the unit
   int64_t begin, count;  // key tiles: the first one's place in the line, how many
   int64_t total;         // the line's length
-  int shares;            // workers that have one
+  int shares;            // into which it is divided
+  int index;             // which of them this is
 };
 
 constexpr int kMaxWorkers = 16;  // of one CTA
 
 struct ShareScratch {
   int64_t warp_sum[32];
-  int64_t bound[kMaxWorkers + 1];
+  int64_t begin[kMaxWorkers], end[kMaxWorkers];
   int64_t weight[kMaxWorkers], rest[kMaxWorkers];
-  int b[kMaxWorkers];
+  int b[kMaxWorkers], index[kMaxWorkers];
 };
 
 // The share of this thread's worker: the CTA has kWorkers, one for each of its first kWorkers
@@ -147,7 +153,7 @@ struct ShareScratch {
 // parallel, by a warp each when there are few of them (a long chunk has many row tiles), by a
 // thread each otherwise.  A share has at least about kMinTiles key tiles: fewer workers take part in
 // a small call.
-template <int kKeys, int kThreads, int kWorkers, int kMinTiles>
+template <int kKeys, int kThreads, int kWorkers, int kMinTiles, bool kPerHead>
 __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& sc) {
   constexpr int kWarps = kThreads / 32;
   static_assert(kWarps <= 32 && kWorkers <= kMaxWorkers && kWorkers <= kWarps, "scratch");
@@ -161,7 +167,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
       const int tiles = row_tiles(p, s);
       for (int rt = by_warp ? lane : 0; rt < tiles; rt += by_warp ? 32 : 1)
         w += unit_tiles<kKeys>(p, s, rt);
-      w *= p.Hk;
+      if (!kPerHead) w *= p.Hk;
     }
     if (by_warp) {
       for (int m = 16; m > 0; m >>= 1) w += __shfl_xor_sync(0xffffffffu, w, m);
@@ -182,10 +188,14 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
     __syncthreads();
     for (int i = 0; i < kWarps; ++i) total += sc.warp_sum[i];
   }
-  const int64_t shares = min(static_cast<int64_t>(p.workers), (total + kMinTiles - 1) / kMinTiles);
-  if (tid <= kWorkers) {  // the borders of this CTA's shares
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * kWorkers + tid;
-    sc.bound[tid] = c < shares ? total * c / shares : total;
+  const int64_t shares =
+      min(static_cast<int64_t>(kPerHead ? p.workers / p.Hk : p.workers), (total + kMinTiles - 1) / kMinTiles);
+  if (tid < kWorkers) {
+    const int g = blockIdx.x * kWorkers + tid;
+    const int64_t c = kPerHead ? g / p.Hk : g;
+    sc.index[tid] = static_cast<int>(c);
+    sc.begin[tid] = c < shares ? total * c / shares : total;
+    sc.end[tid] = c < shares ? total * (c + 1) / shares : total;
   }
   __syncthreads();
   int64_t before = 0;
@@ -206,7 +216,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
     for (int i = 0; i < warp; ++i) lo += sc.warp_sum[i];
     if (mine > 0) {
       for (int w = 0; w < kWorkers; ++w) {
-        const int64_t begin = sc.bound[w];
+        const int64_t begin = sc.begin[w];
         if (begin >= lo && begin < lo + mine) {
           sc.b[w] = b;
           sc.rest[w] = begin - lo;
@@ -219,18 +229,23 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
   __syncthreads();
   const int worker = kWorkers == 1 ? 0 : min(warp, kWorkers - 1);
   Share sh;
-  sh.begin = sc.bound[worker];
-  sh.count = sc.b[worker] < 0 ? 0 : sc.bound[worker + 1] - sh.begin;
+  sh.begin = sc.begin[worker];
+  sh.count = sc.b[worker] < 0 ? 0 : sc.end[worker] - sh.begin;
+  sh.index = sc.index[worker];
   sh.total = total;
   sh.shares = static_cast<int>(shares);
   sh.tile = 0;
   sh.u.b = sc.b[worker];
   if (sh.count > 0) {
     sh.u.s = load_sequence(p, sh.u.b);
-    const int64_t per_head = sc.weight[worker] / p.Hk;
     int64_t rest = sc.rest[worker];
-    sh.u.hk = static_cast<int>(rest / per_head);
-    rest -= sh.u.hk * per_head;
+    if (kPerHead) {
+      sh.u.hk = static_cast<int>(blockIdx.x * kWorkers + worker) % p.Hk;
+    } else {
+      const int64_t per_head = sc.weight[worker] / p.Hk;
+      sh.u.hk = static_cast<int>(rest / per_head);
+      rest -= sh.u.hk * per_head;
+    }
     // the row tile: 32 at a time, each warp for itself
     const int tiles = row_tiles(p, sh.u.s);
     for (int rt0 = 0;; rt0 += 32) {
@@ -254,7 +269,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
   return sh;
 }
 
-// The worker that has the key tile at place x of the line.
+// The share that has the key tile at place x of the line.
 __device__ __forceinline__ int owner(const Share& sh, int64_t x) {
   return static_cast<int>(((x + 1) * sh.shares - 1) / sh.total);
 }
@@ -266,10 +281,10 @@ __device__ __forceinline__ int64_t row_offset(const PagedParams& p, int64_t q0, 
   return (q0 + i) * ld + static_cast<int64_t>(hk * p.G + r - i * p.G) * D;
 }
 
-// What worker c leaves for the joining kernel: parts 0 unless it began the unit and did not
+// What a worker leaves for the joining kernel: parts 0 unless it began the unit and did not
 // finish it.  `at`: the place in the line of its first tile in the unit.
-__device__ __forceinline__ int4 part_unit(const Share& sh, const Unit& u, int c, int64_t at, bool begun_only) {
-  const int parts = begun_only ? owner(sh, at + u.nt - 1) - c + 1 : 0;
+__device__ __forceinline__ int4 part_unit(const Share& sh, const Unit& u, int64_t at, bool begun_only) {
+  const int parts = begun_only ? owner(sh, at + u.nt - 1) - sh.index + 1 : 0;
   return make_int4(static_cast<int>(u.s.q0), u.rt, u.rows, u.hk * 4096 + parts);
 }
 
@@ -277,8 +292,9 @@ __device__ __forceinline__ int4 part_unit(const Share& sh, const Unit& u, int c,
 __device__ __forceinline__ float max_or_nan(float a, float b) { return a != a || a >= b ? a : b; }
 
 // Joins the parts of the units that the kWorkers workers of CTA blockIdx.x began: the worker's last
-// slot, then the first slots of the workers after it; gridDim.y blocks take a unit's rows in turn.
-// (A unit that spans the whole machine has over a thousand parts.)
+// slot, then the first slots of the workers of the next shares of its head.  gridDim.y blocks take
+// the pairs of a worker and a row in turn: a warp each where the unit has up to kJoinWarpParts
+// parts, else a block (a unit that spans the whole machine has over a thousand).
 constexpr int kJoinWarpParts = 32;
 
 template <int D, int kWorkers>
@@ -292,14 +308,14 @@ __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p
   if (threadIdx.x < kWorkers) s_units[threadIdx.x] = p.part_units[blockIdx.x * kWorkers + threadIdx.x];
   __syncthreads();
   // Units of few parts: a warp each, D / 32 columns a lane.
-  static_assert(kWorkers == 8, "a warp per worker");
-  {
+  const int pairs = kWorkers * p.tile_rows;  // of a worker and a row
+  for (int q = blockIdx.y * 8 + (threadIdx.x >> 5); q < pairs; q += 8 * gridDim.y) {
     constexpr int kCols = D / 32;
-    const int w = threadIdx.x >> 5, c = blockIdx.x * kWorkers + w;
+    const int w = q % kWorkers, r = q / kWorkers, c = blockIdx.x * kWorkers + w;
     const int4 un = s_units[w];
     const int parts = un.w & 4095;
-    for (int r = blockIdx.y; parts > 0 && parts <= kJoinWarpParts && r < un.z; r += gridDim.y) {
-      auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.tile_rows + r; };
+    if (parts > 0 && parts <= kJoinWarpParts && r < un.z) {
+      auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i * p.Hk)) * p.tile_rows + r; };
       const float2 mine = lane < parts ? p.part_ml[row_of(lane)] : make_float2(-INFINITY, 0.f);
       float m = mine.x;
       for (int k = 16; k > 0; k >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
@@ -327,57 +343,55 @@ __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p
     }
   }
   // The others: the whole block, slices of the parts side by side.
-  for (int w = 0; w < kWorkers; ++w) {
-    const int c = blockIdx.x * kWorkers + w;
+  for (int q = blockIdx.y; q < pairs; q += gridDim.y) {
+    const int w = q % kWorkers, r = q / kWorkers, c = blockIdx.x * kWorkers + w;
     const int4 un = s_units[w];
     const int parts = un.w & 4095;
-    if (parts <= kJoinWarpParts) continue;
-    auto row_of = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * p.tile_rows + r; };
-    for (int r = blockIdx.y; r < un.z; r += gridDim.y) {
-      float m = -INFINITY;
-      for (int i = threadIdx.x; i < parts; i += 256) m = max_or_nan(m, p.part_ml[row_of(i, r)].x);
-      for (int k = 16; k > 0; k >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
-      if (lane == 0) s_m[threadIdx.x >> 5] = m;
-      __syncthreads();
-      for (int i = 0; i < 8; ++i) m = max_or_nan(m, s_m[i]);
-      const float base = m == -INFINITY ? 0.f : m;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float l = 0.f;
-  #pragma unroll 4
-      for (int i = slice; i < parts; i += kSlices) {
-        const float2 ml = p.part_ml[row_of(i, r)];
-        const float f = exp2f(ml.x - base);
-        l = fmaf(ml.y, f, l);
-        const float4 v = reinterpret_cast<const float4*>(p.part_o)[row_of(i, r) * kGroups + group];
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
-      }
-      s_o[slice][group] = acc;
-      if (group == 0) s_l[slice] = l;
-      __syncthreads();
-      if (slice == 0) {
-        for (int i = 1; i < kSlices; ++i) {
-          const float4 v = s_o[i][group];
-          acc.x += v.x;
-          acc.y += v.y;
-          acc.z += v.z;
-          acc.w += v.w;
-          l += s_l[i];
-        }
-        const float inv = l == 0.f ? 0.f : p.v_scale / l;
-        uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + 4 * group;
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      }
-      __syncthreads();
+    if (parts <= kJoinWarpParts || r >= un.z) continue;
+    auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i * p.Hk)) * p.tile_rows + r; };
+    float m = -INFINITY;
+    for (int i = threadIdx.x; i < parts; i += 256) m = max_or_nan(m, p.part_ml[row_of(i)].x);
+    for (int k = 16; k > 0; k >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
+    if (lane == 0) s_m[threadIdx.x >> 5] = m;
+    __syncthreads();
+    for (int i = 0; i < 8; ++i) m = max_or_nan(m, s_m[i]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int i = slice; i < parts; i += kSlices) {
+      const float2 ml = p.part_ml[row_of(i)];
+      const float f = exp2f(ml.x - base);
+      l = fmaf(ml.y, f, l);
+      const float4 v = reinterpret_cast<const float4*>(p.part_o)[row_of(i) * kGroups + group];
+      acc.x = fmaf(v.x, f, acc.x);
+      acc.y = fmaf(v.y, f, acc.y);
+      acc.z = fmaf(v.z, f, acc.z);
+      acc.w = fmaf(v.w, f, acc.w);
     }
+    s_o[slice][group] = acc;
+    if (group == 0) s_l[slice] = l;
+    __syncthreads();
+    if (slice == 0) {
+      for (int i = 1; i < kSlices; ++i) {
+        const float4 v = s_o[i][group];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        l += s_l[i];
+      }
+      const float inv = l == 0.f ? 0.f : p.v_scale / l;
+      uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + 4 * group;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+    __syncthreads();
   }
 }
 
 // The same for the unit that worker blockIdx.x began, many rows: a block has 8 rows and all
-// groups of four columns; parts are [d / 4][row][4], the
-// layout in which the thread per row that wrote them stored consecutively.
+// groups of four columns; parts are [d / 4][row][4], the layout in which the thread per row that
+// wrote them stored consecutively.
 template <int D, int kRows>
 __global__ void __launch_bounds__(2 * D) paged_join_many_kernel(const PagedParams p) {
   griddep_wait();

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   griddep_launch_dependents();
   griddep_wait();
-  const Share sh = find_share<kKeys, kDecThreads, kDecWarps, kDecMinTiles>(p, scratch);  // has the block's barriers
+  const Share sh = find_share<kKeys, kDecThreads, kDecWarps, kDecMinTiles, true>(p, scratch);  // has the block's barriers
   const int worker = blockIdx.x * kDecWarps + warp;
   if (lane == 0) p.part_units[worker] = make_int4(0, 0, 0, 0);
   if (sh.count == 0) return;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     --lleft;
     if (++ltile == lu.nt && lleft > 0) {
-      next_unit<kKeys>(p, lu);
+      next_unit<kKeys, true>(p, lu);
       ltile = 0;
       // its queries, which are wanted when it begins
       if (lane < lu.rows)
@@ -495,11 +495,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
       }
     }
-    if (lane == 0 && left == n && tile == 0 && n < u.nt) p.part_units[worker] = part_unit(sh, u, worker, at, true);
+    if (lane == 0 && left == n && tile == 0 && n < u.nt) p.part_units[worker] = part_unit(sh, u, at, true);
     left -= n;
     at += n;
     tile = 0;
-    if (left > 0) next_unit<kKeys>(p, u);
+    if (left > 0) next_unit<kKeys, true>(p, u);
   }
   if (!ok) {
     // a timeout: wait for the copies in flight
