@@ -402,7 +402,7 @@ mxq::RopeParams rope_params(const mxq_norm_rope* c, int64_t T, int64_t d) {
   p.rot = static_cast<int>(c->rot);
   p.lanes = 1;
   while (16 * p.lanes < d) p.lanes *= 2;
-  p.pairs = c->style == MXQ_ROPE_PAIRS;
+  p.inv_d = 1.0f / static_cast<float>(d);
   p.row_norm = c->span == MXQ_NORM_ROW;
   return p;
 }
@@ -419,13 +419,53 @@ mxq::RopeOperand rope_operand(const void* x, const void* weight, int64_t ld, voi
   return o;
 }
 
+template <int kCache, bool kPairs>
+mxq_status launch_rope_cache_as(const DeviceInfo& dev, mxq::RopeParams p, const mxq::AppendParams& a,
+                             cudaStream_t stream) {
+  constexpr int kMaxSmem = 224 * 1024;  // of an SM, less what its blocks have statically and as a reserve
+  auto kernel = mxq::rope_cache_kernel<kCache, kPairs>;
+  static PerDevice setup;
+  if (!setup.ensure(dev.index, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) == cudaSuccess;
+      }))
+    return MXQ_ERR_CUDA;
+  const int k_heads = p.k.heads * (kCache ? 2 : 1);
+  const int heads = p.q.heads + k_heads;
+  const int table = p.table ? p.rot * 4 : 0;
+  // Heads per block: all of a token's, or as many as leave a CTA room for two tokens; a norm over
+  // the row keeps each operand whole (at most 128 KB: heads * d <= 2^16).
+  int seg = heads, blocks_y = 1;
+  const int fit = std::max(1, (kMaxSmem / 4 - table) / (p.d * 2));
+  if (heads > fit) {
+    if (p.row_norm) {
+      seg = std::max(p.q.heads, p.k.heads);
+      blocks_y = (p.q.heads ? 1 : 0) + (p.k.heads ? (kCache ? 2 : 1) : 0);
+      p.seg_heads = -1;
+    } else {
+      blocks_y = (heads + fit - 1) / fit;
+      seg = (heads + blocks_y - 1) / blocks_y;
+      p.seg_heads = seg;
+    }
+  }
+  p.stage_bytes = seg * p.d * 2 + table;
+  const int lanes = seg * p.lanes;
+  const int passes = (lanes + mxq::kRopeMaxThreads - 1) / mxq::kRopeMaxThreads;
+  const int threads = std::min(mxq::kRopeMaxThreads, ((seg + passes - 1) / passes * p.lanes + 31) / 32 * 32);
+  // short rows need more CTAs per SM, for the threads
+  const int per_sm = std::min(8, std::max(mxq::kRopeCtas, 1024 / (threads + 32)));
+  p.stages = std::min(mxq::kRopeMaxStages, std::max(1, (kMaxSmem / per_sm - 1024) / p.stage_bytes));
+  const int64_t grid = std::min<int64_t>(p.T, std::max(1, per_sm * dev.sm_count / blocks_y));
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(blocks_y)),
+                          dim3(static_cast<unsigned>(threads + 32)), p.stages * p.stage_bytes, stream, p, a);
+}
+
 template <int kCache>
-mxq_status launch_rope_cache(const mxq::RopeParams& p, const mxq::AppendParams& a, cudaStream_t stream) {
-  const int64_t heads = p.q.heads + static_cast<int64_t>(p.k.heads) * (kCache ? 2 : 1);
-  const int64_t want = (heads * p.lanes + 31) / 32 * 32;
-  const int threads = static_cast<int>(std::min<int64_t>(want, mxq::kRopeMaxThreads));
-  return launch_dependent(mxq::rope_cache_kernel<kCache>, dim3(static_cast<unsigned>(p.T)),
-                          dim3(static_cast<unsigned>(threads)), 0, stream, p, a);
+mxq_status launch_rope_cache(const DeviceInfo& dev, const mxq_norm_rope* cfg, mxq::RopeParams p,
+                             const mxq::AppendParams& a, cudaStream_t stream) {
+  p.inv_q = p.q.heads ? 1.0f / static_cast<float>(p.q.heads * p.d) : 0.f;
+  p.inv_k = p.k.heads ? 1.0f / static_cast<float>(p.k.heads * p.d) : 0.f;
+  return cfg->style == MXQ_ROPE_PAIRS ? launch_rope_cache_as<kCache, true>(dev, p, a, stream)
+                                      : launch_rope_cache_as<kCache, false>(dev, p, a, stream);
 }
 
 // 5-D tensor map over a paged cache: (128-byte piece of a head, token, piece, head, page).
@@ -954,7 +994,7 @@ mxq_status mxq_qk_norm_rope(const mxq_norm_rope* cfg, int64_t T, int64_t d, cons
   p.q = rope_operand(q_bf16, cfg->q_weight, ldq, q_out, ldqo, Hq);
   p.k = rope_operand(k_bf16, cfg->k_weight, ldk, k_out, ldko, Hk);
   p.positions = positions;
-  return launch_rope_cache<0>(p, mxq::AppendParams{}, stream);
+  return launch_rope_cache<0>(dev, cfg, p, mxq::AppendParams{}, stream);
 }
 
 mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* cache, const mxq_paged_batch* batch, int64_t T,
@@ -992,7 +1032,7 @@ mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* cache, co
   a.page_size = static_cast<int>(cache->page_size);
   a.k_inv_scale = 1.0f / cache->k_scale;
   a.v_inv_scale = 1.0f / cache->v_scale;
-  return cache->fmt == MXQ_KV_BF16 ? launch_rope_cache<1>(p, a, stream) : launch_rope_cache<2>(p, a, stream);
+  return cache->fmt == MXQ_KV_BF16 ? launch_rope_cache<1>(dev, cfg, p, a, stream) : launch_rope_cache<2>(dev, cfg, p, a, stream);
 }
 
 int64_t mxq_attention_paged_workspace_bytes(int64_t T, int64_t batch, int64_t Hq, int64_t Hk, int64_t d) {
