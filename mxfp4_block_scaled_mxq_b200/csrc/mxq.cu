@@ -581,7 +581,7 @@ mxq_status launch_paged_chunk(const DeviceInfo& dev, const mxq_paged_kv* c, mxq:
   p.workers = std::min(dev.sm_count, kPagedMaxCtas);
   const int tokens = mxq::kChunkHalf / p.G;  // whole tokens of a half
   p.tile_rows = 2 * tokens * p.G;
-  p.page_box = gcd(p.page_size, kFp8 ? S::kRawKeys : mxq::kChunkKeys);
+  p.page_box = gcd(p.page_size, mxq::kChunkKeys);
   CUtensorMap tq, tk, tv;
   if (!make_tmap_q(&tq, p, D, tokens) || !make_tmap_cache(&tk, c, c->k, p.page_box, false) ||
       !make_tmap_cache(&tv, c, c->v, p.page_box, false))

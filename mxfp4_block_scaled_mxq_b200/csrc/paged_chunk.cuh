@@ -2,26 +2,31 @@
 //
 // A unit is up to 256 rows (two halves of 128 TMEM lanes; whole tokens, so 128 / G * G rows of
 // each half are used) of one key head, against 128 keys per tile.  Roles:
-//   warps 0..7   softmax, a warpgroup per half, one row per thread: scores from TMEM, the running
-//                maximum (raised lazily, by more than 8 in base 2, then the accumulator is rescaled
-//                in TMEM), 2^x, P back to TMEM over the scores, row sums in FP32; at the end
-//                O / l to BF16, or the FP32 part to the workspace.
+//   warps 0..7   softmax, a warpgroup per half, one row per thread: scores from TMEM, 2^x against the
+//                running maximum (which is raised lazily, by more than 8 in base 2, and then the
+//                accumulator is rescaled in TMEM and the weights taken again), P back to TMEM over
+//                the scores, row sums in FP32; at the end O / l to BF16, or the FP32 part to the
+//                workspace.  (Two threads per row, with an exchange of their maxima, took 364 us
+//                where this takes 321: 1560 x 9360 rows x keys, 40 heads.)
 //   warp 8       TMA: Q of the unit once, then K and V tiles in turn, a box per page (zero fill
-//                for pages that are missing or that no row reaches), into a ring.
+//                for pages that are missing or that no row reaches), into rings.
 //   warp 9       MMA: S = Q K^T (128 x 128 x d) and O += P V (P from TMEM, V as the MN-major
 //                operand) of the two halves in turn, so that one half's products run under the
-//                other half's softmax.
-//   warps 10..15 E4M3 cache only: raw tiles to FP16 (which holds E4M3 exactly) in the operand
-//                layout, and Q to FP16, scaled per row by a power of two as in the few-row kernel.
-// Operands and P are BF16, or FP16 with an E4M3 cache.  Bound by the softmax's instructions and
-// the tensor cores, close together.
+//                other half's softmax; P V begins when three quarters of P are there.
+//   warps 12..15 E4M3 cache only: V tiles to FP16 (which holds E4M3 exactly).
+// E4M3 cache: K is used as it is, by kind::f8f6f4 at twice the rate, with every Q row scaled by a
+// power of two and split into two E4M3 terms (four bits each of BF16's eight, so the split is
+// exact down to 2^-14 of the row's largest value and off by 2^-17 of that at most below); P and V are
+// FP16.  BF16 cache: everything is BF16.
+// The scores and the accumulator of both halves fill TMEM, so a half's next scores wait for its
+// P V: its softmax and its products alternate, and their latencies bound the kernel.
 //
 // Every wait is bounded (ptx.cuh); on a timeout the kernel records MXQ_ERR_TIMEOUT, drains
 // its own copies and MMAs, releases TMEM and returns.
 #pragma once
 
-#include "paged_common.cuh"
 #include "attention.cuh"
+#include "paged_common.cuh"
 #include "paged_decode.cuh"
 
 namespace mxq {
@@ -30,11 +35,11 @@ constexpr int kChunkKeys = 128;
 constexpr int kChunkHalf = 128;  // TMEM lanes of a half
 constexpr int kChunkRows = 2 * kChunkHalf;
 constexpr int kChunkSoftWarps = 8;
-constexpr int kChunkMasks = 8;  // tiles whose page masks are kept: more than the ring is ahead
+constexpr int kChunkProducer = 8, kChunkMma = 9, kChunkConv = 12;  // warps
+constexpr int kChunkConvWarps = 4;
+constexpr int kChunkMasks = 8;  // tiles whose page masks are kept: more than the rings are ahead
 constexpr int kChunkMinTiles = 2;
-constexpr int kChunkEarly = 6;     // of a tile's eight 16-key steps: P V begins when these are there
-constexpr int kChunkProducer = 8, kChunkMma = 9, kChunkConv = 10;  // warps
-constexpr int kChunkConvWarps = 6;
+constexpr int kChunkEarly = 6;  // of a tile's eight 16-key steps: P V begins when these are there
 
 template <int D, bool kFp8>
 struct ChunkShape {
@@ -44,39 +49,52 @@ struct ChunkShape {
   static constexpr int kSoftRegs = kFp8 ? 168 : 208;
   static constexpr int kCtrlRegs = kFp8 ? 88 : 80;
   static_assert(256 * kSoftRegs + (kThreads - 256) * kCtrlRegs <= kThreads * kLaunchRegs, "register split");
-  static constexpr int kPieces = D / 64;                        // 128-byte pieces of a BF16 row
-  static constexpr int kPieceBytes = 128 * 128;                 // 128 rows of one piece
-  static constexpr int kQBytes = 2 * kPieces * kPieceBytes;
-  static constexpr int kTileBytes = kPieces * kPieceBytes;      // K or V, BF16
-  static constexpr int kSlots = D == 128 ? (kFp8 ? 4 : 5) : 8;
-  static constexpr int kRawKeys = 64;  // a raw slot: half a tile
-  static constexpr int kRawBytes = kFp8 ? kRawKeys * D : 0;
-  static constexpr int kRawSlots = kFp8 ? (D == 128 ? 3 : 6) : 0;
-  static constexpr int kOffTiles = kQBytes;
-  static constexpr int kOffRaw = kOffTiles + kSlots * kTileBytes;
-  static constexpr int kOffQScale = kOffRaw + kRawSlots * kRawBytes;  // float [2][256], E4M3 only
-  static constexpr int kOffBar = kOffQScale + (kFp8 ? 2048 : 0);
+  static constexpr int kPieces = D / 64;                    // 128-byte pieces of a 16-bit row
+  static constexpr int kPieceBytes = 128 * 128;             // 128 rows of one piece
+  static constexpr int kQHalfBytes = kPieces * kPieceBytes;  // a half's Q: 16 bits, or two E4M3 terms
+  static constexpr int kVBytes = kPieces * kPieceBytes;     // a V tile as operand
+  static constexpr int kKBytes = kFp8 ? kChunkKeys * D : kVBytes;
+  static constexpr int kRawBytes = kFp8 ? kChunkKeys * D : 0;  // a V tile as copied
+  static constexpr int kKSlots = 3, kVSlots = 2, kRawSlots = kFp8 ? 2 : 0;
+  // E4M3: the two terms take the place of the BF16 rows where a row stays in its own bytes
+  // (d = 128: 256 = 2 x 128), else a place of their own
+  static constexpr bool kSplitApart = kFp8 && D == 64;
+  static constexpr int kOffQ = kSplitApart ? 2 * kQHalfBytes : 0;  // Q as operand
+  static constexpr int kOffK = 2 * kQHalfBytes + kOffQ;
+  static constexpr int kOffV = kOffK + kKSlots * kKBytes;
+  static constexpr int kOffRaw = kOffV + kVSlots * kVBytes;
+  static constexpr int kOffQScale = kOffRaw + kRawSlots * kRawBytes;
+  static constexpr int kOffBar = kOffQScale + (kFp8 ? 2 * kChunkRows * 4 : 0);
   static constexpr int kSmemBytes = 1024 + kOffBar + 512;
-  static_assert(kSmemBytes <= 232448 - 512, "shared memory");
+  static_assert(kSmemBytes <= 232448 - 1024, "shared memory");
 };
 
 constexpr uint32_t kChunkTmemCols = 512;
 constexpr uint32_t kChunkColS = 0;    // two halves x 128 columns of scores (P in the first 64 of each)
 constexpr uint32_t kChunkColO = 256;  // two halves x 128 columns of the accumulator
 
-// kind::f16 descriptors: D FP32, A and B both BF16 or both FP16; M 128, N n; b_mn: B is MN-major.
+// Descriptors, D FP32: kind::f16 with A and B both BF16 or both FP16 (kind::f8f6f4 with both
+// E4M3 is all zero in those fields, as FP16 is); M 128, N n; b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t chunk_idesc(int n, bool b_mn, bool bf16) {
-  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (static_cast<uint32_t>(kChunkHalf >> 4) << 24);
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kChunkHalf >> 4) << 24);
 }
 
-__device__ __forceinline__ void tc_mma_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+template <bool kFp8>
+__device__ __forceinline__ void tc_mma_qk(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  if constexpr (kFp8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // A from TMEM.
@@ -103,24 +121,26 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
   using S = ChunkShape<D, kFp8>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;
+  float* q_scale = reinterpret_cast<float*>(smem + S::kOffQScale);  // [unit parity][row], E4M3
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
-  uint64_t* q_ready = q_full + 1;    // E4M3 only: Q is FP16
+  uint64_t* q_ready = q_full + 1;  // E4M3: Q is split
   uint64_t* q_empty = q_ready + 1;
-  uint64_t* s_full = q_empty + 1;    // [2]
-  uint64_t* p_full = s_full + 2;     // [2]
-  uint64_t* p_rest = p_full + 2;     // [2]
-  uint64_t* o_done = p_rest + 2;     // [2]
+  uint64_t* s_full = q_empty + 1;  // [2]
+  uint64_t* p_full = s_full + 2;   // [2] three quarters of P
+  uint64_t* p_rest = p_full + 2;   // [2]
+  uint64_t* o_done = p_rest + 2;   // [2]
   uint64_t* drain = o_done + 2;
-  uint64_t* kv_full = drain + 1;     // [kSlots]
-  uint64_t* kv_empty = kv_full + S::kSlots;
-  uint64_t* raw_full = kv_empty + S::kSlots;  // [kRawSlots]
+  uint64_t* k_full = drain + 1;
+  uint64_t* k_empty = k_full + S::kKSlots;
+  uint64_t* v_full = k_empty + S::kKSlots;
+  uint64_t* v_empty = v_full + S::kVSlots;
+  uint64_t* raw_full = v_empty + S::kVSlots;
   uint64_t* raw_empty = raw_full + S::kRawSlots;
   uint32_t* masks = reinterpret_cast<uint32_t*>(raw_empty + S::kRawSlots);  // [kChunkMasks]
   uint32_t* tmem_slot = masks + kChunkMasks;
-  float* q_scale = reinterpret_cast<float*>(smem + S::kOffQScale);
   __shared__ ShareScratch scratch;
-  auto slot_at = [&](int s) { return smem + S::kOffTiles + s * S::kTileBytes; };
+  auto k_at = [&](int s) { return smem + S::kOffK + s * S::kKBytes; };
+  auto v_at = [&](int s) { return smem + S::kOffV + s * S::kVBytes; };
   auto raw_at = [&](int s) { return smem + S::kOffRaw + s * S::kRawBytes; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -138,9 +158,13 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
       mbar_init(&o_done[t], 1);
     }
     mbar_init(drain, 1);
-    for (int s = 0; s < S::kSlots; ++s) {
-      mbar_init(&kv_full[s], kFp8 ? 2 * kChunkConvWarps : 1);  // the converter's warps, or the copy
-      mbar_init(&kv_empty[s], 1);
+    for (int s = 0; s < S::kKSlots; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < S::kVSlots; ++s) {
+      mbar_init(&v_full[s], kFp8 ? kChunkConvWarps : 1);  // the converter's warps, or the copy
+      mbar_init(&v_empty[s], 1);
     }
     for (int s = 0; s < S::kRawSlots; ++s) {
       mbar_init(&raw_full[s], 1);
@@ -155,7 +179,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
   griddep_launch_dependents();
   griddep_wait();
   const Share sh = find_share<kChunkKeys, S::kThreads, 1, kChunkMinTiles, false>(p, scratch);
-  if (tid == 0 && sh.count == 0) p.part_units[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (tid == 0) p.part_units[blockIdx.x] = make_int4(0, 0, 0, 0);  // nothing to join, also after a timeout
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -170,43 +194,38 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
       int tile = sh.tile;
       int64_t left = sh.count;
       const int nbox = kChunkKeys / p.page_box, box_shift = 31 - __clz(p.page_box);
-      constexpr int kRing = kFp8 ? S::kRawSlots : S::kSlots;
-      uint64_t* full = kFp8 ? raw_full : kv_full;
-      uint64_t* empty = kFp8 ? raw_empty : kv_empty;
-      int slot = 0, units = 0, tiles = 0;
-      uint32_t phase = 0, issued = 0, issued_phase = 0;
+      // rings: 0 K, 1 V (as copied)
+      constexpr int kRing1 = kFp8 ? S::kRawSlots : S::kVSlots;
+      uint64_t* full1 = kFp8 ? raw_full : v_full;
+      uint64_t* empty1 = kFp8 ? raw_empty : v_empty;
+      int slot[2] = {0, 0};
+      uint32_t phase[2] = {0, 0}, issued[2] = {0, 0}, issued_phase[2] = {0, 0};
+      uint32_t units = 0, tiles = 0;
       bool ok = true;
-      int64_t batch_at = -1;  // block-table entries [batch_at, +32) of sequence batch_b in the lanes
-      int batch_b = -1, entries = -1;
+      int batch_at = 0, batch_b = -1, entries = -1;  // block-table entries [batch_at, +32) of sequence batch_b
       while (ok && left > 0) {
         const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
-        const int64_t row = static_cast<int64_t>(u.b) * p.table_stride;
-        if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (units & 1) ^ 1))) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (units & 1) ^ 1));
+        if (!ok) break;
         const int halves = u.rows > half_rows ? 2 : 1;
         if (lane == 0) {
           mbar_arrive_expect_tx(q_full, halves * S::kPieces * half_rows * 128);
           for (int t = 0; t < halves; ++t)
             for (int c = 0; c < S::kPieces; ++c)
-              tma_load_4d(sQ + (t * S::kPieces + c) * S::kPieceBytes, &tmap_q, 0, c, u.hk * p.G,
+              tma_load_4d(smem + t * S::kQHalfBytes + c * S::kPieceBytes, &tmap_q, 0, c, u.hk * p.G,
                           static_cast<int>(u.s.q0) + u.i0 + t * (half_rows / p.G), q_full);
         }
         __syncwarp();
         ++units;
         for (int k = 0; k < n; ++k, ++tiles) {
           const int key0 = (u.kt0 + tile + k) * kChunkKeys;
-          const int box_key = key0 + lane * p.page_box;
-          const int64_t entry = box_key / p.page_size;
-          const int64_t first = key0 / p.page_size;
-          if (batch_b != u.b || batch_at < 0 || first < batch_at || first + nbox > batch_at + 32) {
+          const int first = key0 / p.page_size, box_key = key0 + lane * p.page_box, entry = box_key / p.page_size;
+          if (batch_b != u.b || first < batch_at || first + nbox > batch_at + 32) {
             batch_b = u.b;
             batch_at = first;
-            const int64_t e = first + lane;
-            entries = e < p.table_stride ? p.block_table[row + e] : -1;
+            entries = first + lane < p.table_stride ? p.block_table[u.b * p.table_stride + first + lane] : -1;
           }
-          const int page = __shfl_sync(0xffffffffu, entries, static_cast<int>(min(entry - batch_at, int64_t(31))));
+          const int page = __shfl_sync(0xffffffffu, entries, min(entry - batch_at, 31));
           const bool need = lane < nbox && box_key < u.hi && box_key + p.page_box > u.lo;
           const bool there = need && page >= 0 && page < p.num_pages;
           // the tile's groups of eight keys (boxes hold whole ones) whose page is there
@@ -214,34 +233,35 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           const uint32_t groups =
               __ballot_sync(0xffffffffu, lane < 16 && ((mask >> ((lane * 8) >> box_shift)) & 1u));
           const int pg = there ? page : -1;  // out of range: the box is filled with zeros
-          const int in_page = there ? box_key - static_cast<int>(entry) * p.page_size : 0;
-          constexpr int kCopies = kFp8 ? 4 : 2;  // K, V; E4M3: half tiles (page_box divides them)
+          const int in_page = there ? box_key - entry * p.page_size : 0;
 #pragma unroll
-          for (int v = 0; v < kCopies; ++v) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1))) {
-              ok = false;
-              break;
-            }
-            issued |= 1u << slot;
-            issued_phase = (issued_phase & ~(1u << slot)) | (phase << slot);
+          for (int v = 0; v < 2; ++v) {
+            uint64_t* full = v ? full1 : k_full;
+            uint64_t* empty = v ? empty1 : k_empty;
+            const int s = slot[v];
+            ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], phase[v] ^ 1));
+            if (!ok) break;
+            issued[v] |= 1u << s;
+            issued_phase[v] = (issued_phase[v] & ~(1u << s)) | (phase[v] << s);
             if (lane == 0) {
               if (v == 0) masks[tiles & (kChunkMasks - 1)] = groups;
-              mbar_arrive_expect_tx(&full[slot], kFp8 ? S::kRawBytes : S::kTileBytes);
+              mbar_arrive_expect_tx(&full[s], v ? (kFp8 ? S::kRawBytes : S::kVBytes) : S::kKBytes);
             }
             __syncwarp();
-            if constexpr (kFp8) {
-              const int in_half = lane * p.page_box - (v & 1) * S::kRawKeys;
-              if (in_half >= 0 && in_half < S::kRawKeys)
-                tma_load_5d(raw_at(slot) + in_half * D, v >> 1 ? &tmap_v : &tmap_k, 0, in_page, 0, u.hk, pg, &full[slot]);
-            } else if (lane < nbox) {
+            if (lane < nbox) {
+              const CUtensorMap* m = v ? &tmap_v : &tmap_k;
+              uint8_t* dst = v ? (kFp8 ? raw_at(s) : v_at(s)) : k_at(s);
+              if constexpr (kFp8) {
+                tma_load_5d(dst + lane * p.page_box * D, m, 0, in_page, 0, u.hk, pg, &full[s]);
+              } else {
 #pragma unroll
-              for (int c = 0; c < S::kPieces; ++c)
-                tma_load_5d(slot_at(slot) + c * S::kPieceBytes + lane * p.page_box * 128, v ? &tmap_v : &tmap_k, 0,
-                            in_page, c, u.hk, pg, &full[slot]);
+                for (int c = 0; c < S::kPieces; ++c)
+                  tma_load_5d(dst + c * S::kPieceBytes + lane * p.page_box * 128, m, 0, in_page, c, u.hk, pg, &full[s]);
+              }
             }
-            if (++slot == kRing) {
-              slot = 0;
-              phase ^= 1;
+            if (++slot[v] == (v ? kRing1 : S::kKSlots)) {
+              slot[v] = 0;
+              phase[v] ^= 1;
             }
           }
           if (!ok) break;
@@ -253,8 +273,10 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
       }
       if (!ok) {
         if (units) mbar_wait_drain(q_full, (units - 1) & 1);
-        for (int s = 0; s < kRing; ++s)
-          if (issued & (1u << s)) mbar_wait_drain(&full[s], (issued_phase >> s) & 1u);
+        for (int s = 0; s < S::kKSlots; ++s)
+          if (issued[0] & (1u << s)) mbar_wait_drain(&k_full[s], (issued_phase[0] >> s) & 1u);
+        for (int s = 0; s < kRing1; ++s)
+          if (issued[1] & (1u << s)) mbar_wait_drain(&full1[s], (issued_phase[1] >> s) & 1u);
       }
     } else if (warp == kChunkMma) {
       // ------------------------------------------------------------------ MMA issuer
@@ -263,76 +285,82 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
         int tile = sh.tile;
         int64_t left = sh.count;
         uint32_t units = 0, it[2] = {0, 0};  // tiles issued per half
-        int slot = 0;                        // the ring's next tile (K, V, K, V, ...)
-        uint32_t phase = 0;
+        int k_slot = 0, v_slot = 0;
+        uint32_t k_phase = 0, v_phase = 0;
         bool ok = true;
-        // descriptors: start addresses (16-byte units) are added to these
-        const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024, 2);
-        const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffTiles), 16, 1024, 2);
-        const uint64_t v_desc = smem_desc(smem_u32(smem + S::kOffTiles), S::kPieceBytes, 1024, 2);
-        auto ring_next = [&](int& at) {  // the next tile's slot, once it is full
-          at = slot;
-          const bool full = mbar_wait(&kv_full[slot], phase);
-          if (++slot == S::kSlots) {
-            slot = 0;
-            phase ^= 1;
-          }
-          return full;
-        };
+        // descriptors: start addresses (16-byte units) are added to these; E4M3 rows of 64 bytes
+        // (d = 64) have the 64-byte swizzle
+        constexpr uint32_t kLayout = kFp8 && D == 64 ? 4 : 2, kSbo = kFp8 && D == 64 ? 512 : 1024;
+        const uint64_t q_desc = smem_desc(smem_u32(smem + S::kOffQ), 16, kSbo, kLayout);
+        const uint64_t k_desc = smem_desc(smem_u32(smem + S::kOffK), 16, kSbo, kLayout);
+        const uint64_t v_desc = smem_desc(smem_u32(smem + S::kOffV), S::kPieceBytes, 1024, 2);
         auto issue_qk = [&](int t, int at) {
-          const uint64_t a = q_desc + t * (S::kPieces * S::kPieceBytes >> 4), b = k_desc + at * (S::kTileBytes >> 4);
+          const uint64_t a = q_desc + t * (S::kQHalfBytes >> 4), b = k_desc + at * (S::kKBytes >> 4);
+          const uint32_t d = tmem + kChunkColS + 128 * t;
+          if constexpr (kFp8) {
+            constexpr int kSteps = D / 32;  // of 32 values; then the second terms of Q
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * S::kPieceBytes + (kk & 3) * 32) >> 4;
-            tc_mma_f16(tmem + kChunkColS + 128 * t, a + off, b + off, chunk_idesc(kChunkKeys, false, !kFp8), kk != 0);
+            for (int kk = 0; kk < 2 * kSteps; ++kk)
+              tc_mma_qk<true>(d, a + ((kk / kSteps * kChunkHalf * D + kk % kSteps * 32) >> 4), b + (kk % kSteps * 32 >> 4),
+                              chunk_idesc(kChunkKeys, false, false), kk != 0);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * S::kPieceBytes + (kk & 3) * 32) >> 4;
+              tc_mma_qk<false>(d, a + off, b + off, chunk_idesc(kChunkKeys, false, true), kk != 0);
+            }
           }
           tc_commit(&s_full[t]);
         };
-        auto issue_pv = [&](int t, int at, bool first, int from, int to) {
-          const uint64_t b = v_desc + at * (S::kTileBytes >> 4);
+        // O += P V for the tile's 16-key steps [0, 6), then the rest
+        auto issue_pv = [&](int t, int at, bool rest, bool first) {
+          const uint64_t b = v_desc + at * (S::kVBytes >> 4);
 #pragma unroll
           for (int kk = 0; kk < kChunkKeys / 16; ++kk)
-            if (kk >= from && kk < to)
+            if ((kk >= kChunkEarly) == rest)
               tc_mma_f16_ts(tmem + kChunkColO + 128 * t, tmem + kChunkColS + 128 * t + kk * 8, b + kk * (2048 >> 4),
                             chunk_idesc(D, true, !kFp8), !(first && kk == 0));
         };
         while (ok && left > 0) {
           const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
           const int halves = u.rows > half_rows ? 2 : 1;
-          int ks, vs, next = 0;
-          if (!mbar_wait(kFp8 ? q_ready : q_full, units & 1) || !ring_next(ks)) {
-            ok = false;
-            break;
-          }
+          ok = mbar_wait(kFp8 ? q_ready : q_full, units & 1) && mbar_wait(&k_full[k_slot], k_phase);
+          if (!ok) break;
           tc_fence_after();
-          for (int t = 0; t < halves; ++t) issue_qk(t, ks);
-          tc_commit(&kv_empty[ks]);
+          for (int t = 0; t < halves; ++t) issue_qk(t, k_slot);
+          tc_commit(&k_empty[k_slot]);
           if (n == 1) tc_commit(q_empty);
           for (int k = 0; k < n; ++k) {
             const bool more = k + 1 < n;
-            if (!ring_next(vs) || (more && !ring_next(next))) {
-              ok = false;
-              break;
+            if (++k_slot == S::kKSlots) {
+              k_slot = 0;
+              k_phase ^= 1;
             }
+            ok = mbar_wait(&v_full[v_slot], v_phase) && (!more || mbar_wait(&k_full[k_slot], k_phase));
+            if (!ok) break;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (t >= halves) break;
               ok = mbar_spin(&p_full[t], it[t] & 1);
               if (!ok) break;
               tc_fence_after();
-              issue_pv(t, vs, k == 0, 0, kChunkEarly);
+              issue_pv(t, v_slot, false, k == 0);
               ok = mbar_spin(&p_rest[t], it[t] & 1);
               if (!ok) break;
               ++it[t];
               tc_fence_after();
-              issue_pv(t, vs, false, kChunkEarly, kChunkKeys / 16);
+              issue_pv(t, v_slot, true, false);
               tc_commit(&o_done[t]);
-              if (more) issue_qk(t, next);
+              if (more) issue_qk(t, k_slot);
             }
             if (!ok) break;
-            tc_commit(&kv_empty[vs]);
-            if (more) tc_commit(&kv_empty[next]);
+            tc_commit(&v_empty[v_slot]);
+            if (more) tc_commit(&k_empty[k_slot]);
             if (k + 2 == n) tc_commit(q_empty);
+            if (++v_slot == S::kVSlots) {
+              v_slot = 0;
+              v_phase ^= 1;
+            }
           }
           if (!ok) break;
           ++units;
@@ -346,100 +374,131 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
         }
       }
     } else if (kFp8 && warp >= kChunkConv) {
-      // ------------------------------------------------------------------ converter
+      // ------------------------------------------------------------------ converter of V
       if constexpr (kFp8) {
         constexpr int kThreadsC = 32 * kChunkConvWarps;
         constexpr int kChunks = D / 16;  // 16-value chunks of a row
+        constexpr int kBatch = 4;        // chunks of a thread in flight
         const int ct = tid - 32 * kChunkConv;
+        const int ch = ct % kChunks, key_in = ct / kChunks;
         Unit u = sh.u;
         int tile = sh.tile;
         int64_t left = sh.count;
-        uint32_t units = 0, raw_phase = 0, slot_phase = 1;
-        int rs = 0, ss = 0;
+        uint32_t raw_phase = 0, v_phase = 1, units = 0;
+        int rs = 0, vs = 0;
         bool ok = true;
         while (ok && left > 0) {
           const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
-          // Q: 2^-e x row with the row's largest value in [1, 2) 2^e (rows with |e| > 100 as they are);
-          // exact for BF16's 8 bits down to 2^-14 of that value
+          // Q, under the last tile and the end of the unit before: 2^(7 - e) x row with the row's largest
+          // value in [1, 2) 2^e, as two E4M3 terms (below 2^-119 zeros; a row with Inf gets a NaN scale, since
+          // E4M3 has none).  The scales' slot was read by the softmax two units ago.
           ok = __all_sync(0xffffffffu, mbar_wait(q_full, units & 1));
           if (!ok) break;
-          for (int i = ct; i < min(u.rows, kChunkRows); i += kThreadsC) {
-            const int t = i >= half_rows, r = i - t * half_rows;
-            uint8_t* row = sQ + t * S::kPieces * S::kPieceBytes + r * 128;
+#pragma unroll 1
+          for (int t = 0; t < (u.rows > half_rows ? 2 : 1); ++t) {
+            const int r = ct;  // a thread per row
+            const uint8_t* src = smem + t * S::kQHalfBytes + r * 128;
+            auto piece = [&](int i) {
+              return *reinterpret_cast<const uint4*>(src + (i >> 3) * S::kPieceBytes + (((i & 7) ^ (r & 7)) << 4));
+            };
             float big = 0.f;
 #pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-              const uint4 w = *reinterpret_cast<const uint4*>(row + (c >> 3) * S::kPieceBytes + (((c & 7) ^ (r & 7)) << 4));
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 w = piece(i);
               const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 big = fmaxf(big, fmaxf(fabsf(__uint_as_float(x[j] << 16)), fabsf(__uint_as_float(x[j] & 0xffff0000u))));
             }
             const int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-            const bool fits = e >= -100 && e <= 100;
-            const float down = fits ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
+            const bool fits = e >= -119 && e <= 127;
+            const float down = fits ? __uint_as_float(static_cast<uint32_t>(134 - e) << 23) : 1.f;
             q_scale[(units & 1) * kChunkRows + t * kChunkHalf + r] =
-                fits ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : 1.f;
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-              uint4* at = reinterpret_cast<uint4*>(row + (c >> 3) * S::kPieceBytes + (((c & 7) ^ (r & 7)) << 4));
-              const uint4 w = *at;
-              const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-              uint32_t h[4];
+                fits ? __uint_as_float(static_cast<uint32_t>(120 + e) << 23) : e == 128 ? NAN : 1.f;
+            // Rows of D bytes; the first terms' tile, then the second terms'.  In place (d = 128) these go
+            // over the row's two pieces: what would go over values not yet read is held back.
+            const int sw = D == 128 ? (r & 7) : ((r >> 1) & 3);
+            uint8_t* dst = smem + S::kOffQ + t * S::kQHalfBytes + r * D;
+            uint4 first[D / 16], held[D == 128 ? 4 : 1];
+            auto split = [&](int j) {  // values [16 j, +16): their first terms stay, the second come back
+              uint32_t hi[4], lo[4];
+              const uint4 w2[2] = {piece(2 * j), piece(2 * j + 1)};
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                h[j] = pack_f16x2(__uint_as_float(x[j] << 16) * down, __uint_as_float(x[j] & 0xffff0000u) * down);
-              *at = make_uint4(h[0], h[1], h[2], h[3]);
+              for (int k = 0; k < 4; ++k) {
+                const uint4& ww = w2[k >> 1];
+                const uint32_t x0 = k & 1 ? ww.z : ww.x, x1 = k & 1 ? ww.w : ww.y;
+                const float f[4] = {__uint_as_float(x0 << 16) * down, __uint_as_float(x0 & 0xffff0000u) * down,
+                                    __uint_as_float(x1 << 16) * down, __uint_as_float(x1 & 0xffff0000u) * down};
+                hi[k] = e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16);
+                const uint2 b = e4m3x4_to_f16(hi[k]);
+                const float2 b0 = __half22float2(*reinterpret_cast<const __half2*>(&b.x));
+                const float2 b1 = __half22float2(*reinterpret_cast<const __half2*>(&b.y));
+                lo[k] = e4m3x2(f[0] - b0.x, f[1] - b0.y) | (e4m3x2(f[2] - b1.x, f[3] - b1.y) << 16);
+              }
+              first[j] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              return make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            };
+            auto write = [&](int j, int term, const uint4& w) {
+              *reinterpret_cast<uint4*>(dst + term * kChunkHalf * D + ((j ^ sw) << 4)) = w;
+            };
+            if constexpr (D == 128) {
+#pragma unroll
+              for (int j = 4; j < 8; ++j) held[j - 4] = split(j);
+#pragma unroll
+              for (int j = 4; j < 8; ++j) write(j, 1, held[j - 4]);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) write(j, 1, split(j));
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) write(j, 0, first[j]);
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(q_ready);
           ++units;
-          for (int k = 0; k < 4 * n; ++k) {  // half tiles: K, K, V, V
-            ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], raw_phase) && mbar_wait(&kv_empty[ss], slot_phase));
+          for (int k = 0; k < n; ++k) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], raw_phase) && mbar_wait(&v_empty[vs], v_phase));
             if (!ok) break;
-            const int half0 = (k & 1) * S::kRawKeys;
-            const int key0 = (u.kt0 + tile + (k >> 2)) * kChunkKeys + half0;
-            const bool edge = (k & 2) && (key0 < u.lo || key0 + S::kRawKeys > u.hi);
+            const int key0 = (u.kt0 + tile + k) * kChunkKeys;
+            const bool edge = key0 < u.lo || key0 + kChunkKeys > u.hi;
             const uint8_t* src = raw_at(rs);
-            uint8_t* dst = slot_at(ss) + half0 * 128;
-            constexpr int kSteps = (S::kRawKeys * kChunks + kThreadsC - 1) / kThreadsC;
-            uint4 w[kSteps];
+            uint8_t* dst = v_at(vs) + (ch >> 2) * S::kPieceBytes;
+            const int flip = D == 128 ? ch >> 2 : 0;  // the two pieces' chunks in turn: no bank conflict
+            const int c0 = 2 * (ch & 3);
+            constexpr int kStep = kThreadsC / kChunks;  // keys per pass
+#pragma unroll 1
+            for (int i = key_in; i < kChunkKeys; i += kBatch * kStep) {
+              uint4 w[kBatch];
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
-              const int i = ct + j * kThreadsC, ch = i % kChunks, key = i / kChunks;
-              const int sw = D == 128 ? (key & 7) : ((key >> 1) & 3);
-              if (key < S::kRawKeys) w[j] = *reinterpret_cast<const uint4*>(src + key * D + ((ch ^ sw) << 4));
-              // values of keys that no row of the unit attends may be anything: 0 x NaN is NaN
-              if (edge && (key0 + key < u.lo || key0 + key >= u.hi)) w[j] = make_uint4(0, 0, 0, 0);
-            }
+              for (int j = 0; j < kBatch; ++j) {
+                const int key = i + j * kStep, sw = D == 128 ? (key & 7) : ((key >> 1) & 3);
+                w[j] = *reinterpret_cast<const uint4*>(src + key * D + ((ch ^ sw) << 4));
+                // values of keys that no row of the unit attends may be anything: 0 x NaN is NaN
+                if (edge && (key0 + key < u.lo || key0 + key >= u.hi)) w[j] = make_uint4(0, 0, 0, 0);
+              }
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j) {
-              const int i = ct + j * kThreadsC, ch = i % kChunks, key = i / kChunks;
-              if (key >= S::kRawKeys) break;
-              const uint2 a = e4m3x4_to_f16(w[j].x), b = e4m3x4_to_f16(w[j].y), c = e4m3x4_to_f16(w[j].z),
-                          d = e4m3x4_to_f16(w[j].w);
-              const uint4 v0 = make_uint4(a.x, a.y, b.x, b.y), v1 = make_uint4(c.x, c.y, d.x, d.y);
-              const int flip = D == 128 ? ch >> 2 : 0;  // the two pieces' chunks in turn: no bank conflict
-              const int c0 = 2 * (ch & 3);
-              uint8_t* to = dst + (ch >> 2) * S::kPieceBytes + key * 128;
-              *reinterpret_cast<uint4*>(to + (((c0 + flip) ^ (key & 7)) << 4)) = flip ? v1 : v0;
-              *reinterpret_cast<uint4*>(to + (((c0 + 1 - flip) ^ (key & 7)) << 4)) = flip ? v0 : v1;
+              for (int j = 0; j < kBatch; ++j) {
+                const int key = i + j * kStep;
+                const uint2 a = e4m3x4_to_f16(w[j].x), b = e4m3x4_to_f16(w[j].y), c = e4m3x4_to_f16(w[j].z),
+                            d = e4m3x4_to_f16(w[j].w);
+                const uint4 x0 = make_uint4(a.x, a.y, b.x, b.y), x1 = make_uint4(c.x, c.y, d.x, d.y);
+                *reinterpret_cast<uint4*>(dst + key * 128 + (((c0 + flip) ^ (key & 7)) << 4)) = flip ? x1 : x0;
+                *reinterpret_cast<uint4*>(dst + key * 128 + (((c0 + 1 - flip) ^ (key & 7)) << 4)) = flip ? x0 : x1;
+              }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              mbar_arrive(&kv_full[ss]);
+              mbar_arrive(&v_full[vs]);
               mbar_arrive(&raw_empty[rs]);
             }
             if (++rs == S::kRawSlots) {
               rs = 0;
               raw_phase ^= 1;
             }
-            if ((k & 1) && ++ss == S::kSlots) {
-              ss = 0;
-              slot_phase ^= 1;
+            if (++vs == S::kVSlots) {
+              vs = 0;
+              v_phase ^= 1;
             }
           }
           left -= n;
@@ -465,11 +524,11 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
       const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
       const int row = t * half_rows + r;  // of the unit
       const bool live = r < half_rows && row < u.rows;
+      float scale = p.scale_log2;
       float m = -INFINITY, l = 0.f;
       if (t == 0 || u.rows > half_rows) {
         const int tok = (u.r0 + min(row, u.rows - 1)) / p.G;
         const int2 kr = key_range(p, u.s, tok, tok);
-        float scale = p.scale_log2;
         for (int k = 0; k < n; ++k, ++it) {
           const int key0 = (u.kt0 + tile + k) * kChunkKeys;
           ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], it & 1));
@@ -477,6 +536,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           tc_fence_after();
           float s[128];
           auto load = [&](int c) { tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c])); };
+          if (kFp8 && k == 0) scale *= q_scale[(units & 1) * kChunkRows + t * kChunkHalf + r];
           auto mask = [&](int c, uint32_t there) {
             // bit i of on: key 32 c + i is attended
             const int lo = min(max(kr.x - key0 - 32 * c, 0), 32), hi = min(max(kr.y - key0 - 32 * c, 0), 32);
@@ -489,13 +549,12 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           };
           load(0);
           load(1);
-          if (kFp8 && k == 0) scale = p.scale_log2 * q_scale[(units & 1) * kChunkRows + t * kChunkHalf + r];
+          load(2);
+          load(3);
           const uint32_t there = masks[(g + k) & (kChunkMasks - 1)];
           const bool masked =
               __any_sync(0xffffffffu, key0 < kr.x || key0 + kChunkKeys > kr.y || there != 0xffffu);
           tmem_ld_wait();
-          load(2);
-          load(3);
           auto arrive = [&](uint64_t* bar) {
             tmem_st_wait();
             tc_fence_before();
@@ -532,24 +591,17 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
             if (with_mask) {
               mask(0, there);
               mask(1, there);
+              mask(2, there);
+              mask(3, there);
             }
             float m4[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               m4[q] = fmax3_nan(s[q], s[q + 4], s[q + 4]);
 #pragma unroll
-              for (int i = 8 + q; i < 64; i += 8) m4[q] = fmax3_nan(m4[q], s[i], s[i + 4]);
+              for (int i = 8 + q; i < 128; i += 8) m4[q] = fmax3_nan(m4[q], s[i], s[i + 4]);
             }
             weights(0);
-            tmem_ld_wait();
-            if (with_mask) {
-              mask(2, there);
-              mask(3, there);
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int i = 64 + q; i < 128; i += 8) m4[q] = fmax3_nan(m4[q], s[i], s[i + 4]);
             float mx = fmax3_nan(fmax3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]) * scale;
             if (mx == INFINITY) mx = NAN;
             // raised when it would let P pass 2^8 (and when a score is NaN: then the row's maximum, sum
@@ -596,16 +648,16 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           if (masked) {
             if (!kFp8 && t == 0 && (key0 < u.lo || key0 + kChunkKeys > u.hi)) {
               // values of keys that no row of the unit attends may be anything: 0 x NaN is NaN
-              const uint32_t i = 2 * (g + k) + 1;
-              const int sl = static_cast<int>(i % S::kSlots);
-              ok = __all_sync(0xffffffffu, mbar_wait(&kv_full[sl], (i / S::kSlots) & 1));
+              const uint32_t i = g + k;
+              const int sl = static_cast<int>(i % S::kVSlots);
+              ok = __all_sync(0xffffffffu, mbar_wait(&v_full[sl], (i / S::kVSlots) & 1));
               if (!ok) break;
               if (key0 + r < u.lo || key0 + r >= u.hi) {
 #pragma unroll
                 for (int c = 0; c < S::kPieces; ++c)
 #pragma unroll
                   for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<uint4*>(slot_at(sl) + c * S::kPieceBytes + r * 128 + q * 16) =
+                    *reinterpret_cast<uint4*>(v_at(sl) + c * S::kPieceBytes + r * 128 + q * 16) =
                         make_uint4(0, 0, 0, 0);
               }
               fence_proxy_async_smem();
@@ -639,10 +691,10 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t v[32];
+            __syncwarp();  // rows that are not there have skipped the stores below
             tmem_ld32(tO + 32 * c, v);
             tmem_ld_wait();
-            if (!live) continue;
-            if (whole) {
+            if (live && whole) {
               uint32_t w[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i)
@@ -656,7 +708,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
                   *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) =
                       make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
               }
-            } else {
+            } else if (live) {
 #pragma unroll
               for (int q = 0; q < 8; ++q)
                 part[(8 * c + q) * kChunkRows] =
@@ -665,10 +717,11 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
             }
           }
           if (live && !whole) p.part_ml[part_slot * kChunkRows + row] = make_float2(m, l);
+          __syncwarp();
           tc_fence_before();
         }
       }
-      if (tid == 0 && left == n)
+      if (ok && tid == 0 && left == n)
         p.part_units[blockIdx.x] = part_unit(sh, u, at, tile == 0 && n < u.nt);
       g += n;
       ++units;

@@ -227,9 +227,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        // 2^-e with the row's largest value in [1, 2) 2^e; rows outside |e| <= 100 are left as they are
-        const int e = static_cast<int>(__float_as_uint(big) >> 23) - 127;
-        const bool fits = e >= -100 && e <= 100;
+        // 2^-e with the row's largest value in [1, 2) 2^e (or [2, 4) 2^126); Inf and subnormals as they are
+        const int e = min(static_cast<int>(__float_as_uint(big) >> 23) - 127, 126);
+        const bool fits = e >= -126 && big != INFINITY;
         const float down = fits ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
         const float up = fits ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : p.scale_log2;
 #pragma unroll

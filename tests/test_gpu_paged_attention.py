@@ -198,11 +198,11 @@ def test_peaked_and_flat_scores(n, fp8, spread):
 
 @pytest.mark.parametrize("n", [1, 150])
 def test_scales_of_q_at_the_ends_of_the_type(n):
-    """An E4M3 cache with queries of about 2^90 and 2^-90, the softmax scale undoing it."""
+    """An E4M3 cache with queries of about 2^110 and 2^-110, the softmax scale undoing it."""
     s = make([n], [300], 8, 2, 128, 16, True, seed=13)
     base = s["q"].clone()
     want = call(s, scale=2.0 ** -4)
-    for e in (90, -90):
+    for e in (90, -90, 110, -110):
         s["q"] = base * 2.0 ** e
         assert torch.equal(call(s, scale=2.0 ** (-4 - e)), want)
 
