@@ -8,7 +8,8 @@
 //                the scores, row sums in FP32; at the end O / l to BF16, or the FP32 part to the
 //                workspace.  (Two threads per row, with an exchange of their maxima, took 364 us
 //                where this takes 321: 1560 x 9360 rows x keys, 40 heads.)
-//   warp 8       TMA: Q of the unit once, then K and V tiles in turn, a box per page (zero fill
+//   warp 8       takes the CTA's share apart into segments of units for the others (through shared
+//                memory: carried by every thread, a unit's bounds cost the softmax registers); TMA: Q of the unit once, then K and V tiles in turn, a box per page (zero fill
 //                for pages that are missing or that no row reaches), into rings.
 //   warp 9       MMA: S = Q K^T (128 x 128 x d) and O += P V (P from TMEM, V as the MN-major
 //                operand) of the two halves in turn, so that one half's products run under the
@@ -46,8 +47,8 @@ struct ChunkShape {
   static constexpr int kThreads = kFp8 ? 512 : 384;
   // registers a thread: at launch, softmax warps, the other warps
   static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
-  static constexpr int kSoftRegs = kFp8 ? 168 : 208;
-  static constexpr int kCtrlRegs = kFp8 ? 88 : 80;
+  static constexpr int kSoftRegs = kFp8 ? 168 : 216;
+  static constexpr int kCtrlRegs = kFp8 ? 88 : 72;
   static_assert(256 * kSoftRegs + (kThreads - 256) * kCtrlRegs <= kThreads * kLaunchRegs, "register split");
   static constexpr int kPieces = D / 64;                    // 128-byte pieces of a 16-bit row
   static constexpr int kPieceBytes = 128 * 128;             // 128 rows of one piece
@@ -67,6 +68,15 @@ struct ChunkShape {
   static constexpr int kOffBar = kOffQScale + (kFp8 ? 2 * kChunkRows * 4 : 0);
   static constexpr int kSmemBytes = 1024 + kOffBar + 512;
   static_assert(kSmemBytes <= 232448 - 1024, "shared memory");
+};
+
+// A segment of a unit as the producer hands it on.
+struct ChunkUnit {
+  int tiles;  // 0: no more
+  int key0;   // of the first tile
+  int lo, hi, rows, r0, hk;
+  Sequence s;
+  int whole, slot;  // all of the unit; else which of the CTA's two slots its part goes to
 };
 
 constexpr uint32_t kChunkTmemCols = 512;
@@ -130,7 +140,9 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
   uint64_t* p_rest = p_full + 2;   // [2]
   uint64_t* o_done = p_rest + 2;   // [2]
   uint64_t* drain = o_done + 2;
-  uint64_t* k_full = drain + 1;
+  uint64_t* unit_full = drain + 1;  // [2]
+  uint64_t* unit_empty = unit_full + 2;
+  uint64_t* k_full = unit_empty + 2;
   uint64_t* k_empty = k_full + S::kKSlots;
   uint64_t* v_full = k_empty + S::kKSlots;
   uint64_t* v_empty = v_full + S::kVSlots;
@@ -139,6 +151,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
   uint32_t* masks = reinterpret_cast<uint32_t*>(raw_empty + S::kRawSlots);  // [kChunkMasks]
   uint32_t* tmem_slot = masks + kChunkMasks;
   __shared__ ShareScratch scratch;
+  __shared__ ChunkUnit chunk_units[2];
   auto k_at = [&](int s) { return smem + S::kOffK + s * S::kKBytes; };
   auto v_at = [&](int s) { return smem + S::kOffV + s * S::kVBytes; };
   auto raw_at = [&](int s) { return smem + S::kOffRaw + s * S::kRawBytes; };
@@ -158,6 +171,10 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
       mbar_init(&o_done[t], 1);
     }
     mbar_init(drain, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&unit_full[s], 1);
+      mbar_init(&unit_empty[s], kChunkSoftWarps + 1 + (kFp8 ? kChunkConvWarps : 0));
+    }
     for (int s = 0; s < S::kKSlots; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
@@ -192,7 +209,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
       // ------------------------------------------------------------------ TMA producer
       Unit u = sh.u;
       int tile = sh.tile;
-      int64_t left = sh.count;
+      int64_t left = sh.count, at = sh.begin;
       const int nbox = kChunkKeys / p.page_box, box_shift = 31 - __clz(p.page_box);
       // rings: 0 K, 1 V (as copied)
       constexpr int kRing1 = kFp8 ? S::kRawSlots : S::kVSlots;
@@ -205,6 +222,23 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
       int batch_at = 0, batch_b = -1, entries = -1;  // block-table entries [batch_at, +32) of sequence batch_b
       while (ok && left > 0) {
         const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
+        ok = __all_sync(0xffffffffu, mbar_wait(&unit_empty[units & 1], ((units >> 1) & 1) ^ 1));
+        if (!ok) break;
+        if (lane == 0) {
+          ChunkUnit& c = chunk_units[units & 1];
+          c.tiles = n;
+          c.key0 = (u.kt0 + tile) * kChunkKeys;
+          c.lo = u.lo;
+          c.hi = u.hi;
+          c.rows = u.rows;
+          c.r0 = u.r0;
+          c.hk = u.hk;
+          c.s = u.s;
+          c.whole = tile == 0 && n == u.nt;
+          c.slot = tile == 0 ? 1 : 0;
+          mbar_arrive(&unit_full[units & 1]);
+          if (left == n) p.part_units[blockIdx.x] = part_unit(sh, u, at, tile == 0 && n < u.nt);
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (units & 1) ^ 1));
         if (!ok) break;
         const int halves = u.rows > half_rows ? 2 : 1;
@@ -268,8 +302,13 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
         }
         if (!ok) break;
         left -= n;
+        at += n;
         tile = 0;
         if (left > 0) next_unit<kChunkKeys, false>(p, u);
+      }
+      if (ok && __all_sync(0xffffffffu, mbar_wait(&unit_empty[units & 1], ((units >> 1) & 1) ^ 1)) && lane == 0) {
+        chunk_units[units & 1].tiles = 0;
+        mbar_arrive(&unit_full[units & 1]);
       }
       if (!ok) {
         if (units) mbar_wait_drain(q_full, (units - 1) & 1);
@@ -281,9 +320,6 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
     } else if (warp == kChunkMma) {
       // ------------------------------------------------------------------ MMA issuer
       if (elect_one()) {
-        Unit u = sh.u;
-        int tile = sh.tile;
-        int64_t left = sh.count;
         uint32_t units = 0, it[2] = {0, 0};  // tiles issued per half
         int k_slot = 0, v_slot = 0;
         uint32_t k_phase = 0, v_phase = 0;
@@ -321,9 +357,13 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
               tc_mma_f16_ts(tmem + kChunkColO + 128 * t, tmem + kChunkColS + 128 * t + kk * 8, b + kk * (2048 >> 4),
                             chunk_idesc(D, true, !kFp8), !(first && kk == 0));
         };
-        while (ok && left > 0) {
-          const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
-          const int halves = u.rows > half_rows ? 2 : 1;
+        for (;;) {
+          ok = mbar_wait(&unit_full[units & 1], (units >> 1) & 1);
+          if (!ok) break;
+          const int n = chunk_units[units & 1].tiles;
+          if (n == 0) break;
+          const int halves = chunk_units[units & 1].rows > half_rows ? 2 : 1;
+          mbar_arrive(&unit_empty[units & 1]);
           ok = mbar_wait(kFp8 ? q_ready : q_full, units & 1) && mbar_wait(&k_full[k_slot], k_phase);
           if (!ok) break;
           tc_fence_after();
@@ -364,9 +404,6 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           }
           if (!ok) break;
           ++units;
-          left -= n;
-          tile = 0;
-          if (left > 0) next_unit<kChunkKeys, false>(p, u);
         }
         if (!ok) {
           tc_commit(drain);
@@ -381,14 +418,14 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
         constexpr int kBatch = 4;        // chunks of a thread in flight
         const int ct = tid - 32 * kChunkConv;
         const int ch = ct % kChunks, key_in = ct / kChunks;
-        Unit u = sh.u;
-        int tile = sh.tile;
-        int64_t left = sh.count;
         uint32_t raw_phase = 0, v_phase = 1, units = 0;
         int rs = 0, vs = 0;
-        bool ok = true;
-        while (ok && left > 0) {
-          const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
+        for (bool ok = true; ok; ++units) {
+          const ChunkUnit& u = chunk_units[units & 1];
+          ok = __all_sync(0xffffffffu, mbar_wait(&unit_full[units & 1], (units >> 1) & 1));
+          if (!ok) break;
+          const int n = u.tiles;
+          if (n == 0) break;
           // Q, under the last tile and the end of the unit before: 2^(7 - e) x row with the row's largest
           // value in [1, 2) 2^e, as two E4M3 terms (below 2^-119 zeros; a row with Inf gets a NaN scale, since
           // E4M3 has none).  The scales' slot was read by the softmax two units ago.
@@ -455,11 +492,10 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(q_ready);
-          ++units;
           for (int k = 0; k < n; ++k) {
             ok = __all_sync(0xffffffffu, mbar_wait(&raw_full[rs], raw_phase) && mbar_wait(&v_empty[vs], v_phase));
             if (!ok) break;
-            const int key0 = (u.kt0 + tile + k) * kChunkKeys;
+            const int key0 = u.key0 + k * kChunkKeys;
             const bool edge = key0 < u.lo || key0 + kChunkKeys > u.hi;
             const uint8_t* src = raw_at(rs);
             uint8_t* dst = v_at(vs) + (ch >> 2) * S::kPieceBytes;
@@ -501,9 +537,8 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
               v_phase ^= 1;
             }
           }
-          left -= n;
-          tile = 0;
-          if (ok && left > 0) next_unit<kChunkKeys, false>(p, u);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&unit_empty[units & 1]);
         }
       }
     }
@@ -514,14 +549,15 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
     const int r = (warp & 3) * 32 + lane;  // TMEM lane: row of the half
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + kChunkColS + 128 * t, tO = tmem + lane_off + kChunkColO + 128 * t;
-    Unit u = sh.u;
-    int tile = sh.tile;
-    int64_t left = sh.count, at = sh.begin;
     uint32_t it = 0, units = 0;
     uint32_t g = 0;  // tiles of all units so far
     bool ok = true;
-    while (ok && left > 0) {
-      const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
+    for (;; ++units) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&unit_full[units & 1], (units >> 1) & 1));
+      if (!ok) break;
+      const ChunkUnit& u = chunk_units[units & 1];
+      const int n = u.tiles;
+      if (n == 0) break;
       const int row = t * half_rows + r;  // of the unit
       const bool live = r < half_rows && row < u.rows;
       float scale = p.scale_log2;
@@ -529,8 +565,8 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
       if (t == 0 || u.rows > half_rows) {
         const int tok = (u.r0 + min(row, u.rows - 1)) / p.G;
         const int2 kr = key_range(p, u.s, tok, tok);
-        for (int k = 0; k < n; ++k, ++it) {
-          const int key0 = (u.kt0 + tile + k) * kChunkKeys;
+        int key0 = u.key0;
+        for (int k = 0; k < n; ++k, ++it, key0 += kChunkKeys) {
           ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], it & 1));
           if (!ok) break;
           tc_fence_after();
@@ -682,9 +718,9 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[t], (it - 1) & 1));
         if (ok) {
           tc_fence_after();
-          const bool whole = tile == 0 && n == u.nt;
+          const bool whole = u.whole != 0;
           const float inv = l == 0.f ? 0.f : p.v_scale / l;
-          const int64_t part_slot = 2 * static_cast<int64_t>(blockIdx.x) + (tile == 0 ? 1 : 0);
+          const int64_t part_slot = 2 * static_cast<int64_t>(blockIdx.x) + u.slot;
           uint16_t* dst = p.out + row_offset<D>(p, u.s.q0, u.hk, u.r0 + (live ? row : 0), p.ldo);
           // parts: [four columns][row], so that a warp's stores are consecutive
           float4* part = reinterpret_cast<float4*>(p.part_o) + part_slot * (D / 4) * kChunkRows + row;
@@ -721,14 +757,10 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           tc_fence_before();
         }
       }
-      if (ok && tid == 0 && left == n)
-        p.part_units[blockIdx.x] = part_unit(sh, u, at, tile == 0 && n < u.nt);
+      if (!ok) break;
       g += n;
-      ++units;
-      left -= n;
-      at += n;
-      tile = 0;
-      if (ok && left > 0) next_unit<kChunkKeys, false>(p, u);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&unit_empty[units & 1]);
     }
   }
   tc_fence_before();
