@@ -506,15 +506,16 @@ PagedWorkspace paged_workspace(int tile_rows, int64_t d) {
   return w;
 }
 
-// Which kernel, by the rows that share a key head: the few-row one streams the cache once per row tile
-// of 8, 16 or 32 rows, the other computes 256 whether they are there or not.  By the mean over the
-// sequences, since the lengths are on the device: every kernel is right for any.
-int paged_tile_rows(int64_t T, int64_t batch, int64_t G, int64_t d) {
+// Which kernel, by the rows that share a key head: the few-row one streams the cache once per row tile of
+// 8 or 16 rows, the other computes 256 whether they are there or not.  24 sequences of 4000 keys,
+// 8 key heads, d = 128, BF16 (E4M3): 16 rows 85 (65) us against some 98 (103) us, 32 rows 100 (93)
+// against 98 (103), 48 rows 136 (125) against 100 (104); four sequences of 1000 keys: 32 rows 28 (25)
+// against 18 (20).  By the mean over the sequences, since the lengths are on the device: every
+// kernel is right for any.
+int paged_tile_rows(int64_t T, int64_t batch, int64_t G) {
   const int64_t rows = (T * G + batch - 1) / batch;
   if (rows <= 8) return 8;
-  if (rows <= 16) return 16;
-  if ((d == 64 && rows <= 32) || G > mxq::kChunkHalf) return d == 64 ? 32 : 16;
-  return mxq::kChunkRows;
+  return rows <= 16 || G > mxq::kChunkHalf ? 16 : mxq::kChunkRows;
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -541,15 +542,6 @@ mxq_status launch_paged_decode(const DeviceInfo& dev, const mxq_paged_kv* c, mxq
   return launch_dependent(mxq::paged_join_few_kernel<D, mxq::kDecWarps>,
                           dim3(static_cast<unsigned>(ctas), 8), dim3(256), 0,
                           stream, p);
-}
-
-template <int D, bool kFp8>
-mxq_status launch_paged_few(const DeviceInfo& dev, const mxq_paged_kv* c, const mxq::PagedParams& p,
-                            cudaStream_t stream) {
-  if (p.tile_rows == 8) return launch_paged_decode<D, kFp8, 1>(dev, c, p, stream);
-  if constexpr (D == 64)
-    if (p.tile_rows == 32) return launch_paged_decode<D, kFp8, 4>(dev, c, p, stream);
-  return launch_paged_decode<D, kFp8, 2>(dev, c, p, stream);
 }
 
 // Q as (128-byte piece, piece, head, token): a box is one piece of the G heads of whole tokens.
@@ -591,6 +583,13 @@ mxq_status launch_paged_chunk(const DeviceInfo& dev, const mxq_paged_kv* c, mxq:
   if (st != MXQ_OK) return st;
   return launch_dependent(mxq::paged_join_many_kernel<D, mxq::kChunkRows>,
                           dim3(static_cast<unsigned>(p.workers), mxq::kChunkRows / 8), dim3(2 * D), 0, stream, p);
+}
+
+template <int D, bool kFp8>
+mxq_status launch_paged(const DeviceInfo& dev, const mxq_paged_kv* c, const mxq::PagedParams& p, cudaStream_t stream) {
+  if (p.tile_rows == mxq::kChunkRows) return launch_paged_chunk<D, kFp8>(dev, c, p, stream);
+  return p.tile_rows == 8 ? launch_paged_decode<D, kFp8, 1>(dev, c, p, stream)
+                          : launch_paged_decode<D, kFp8, 2>(dev, c, p, stream);
 }
 
 }  // namespace
@@ -1037,7 +1036,7 @@ mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* cache, co
 
 int64_t mxq_attention_paged_workspace_bytes(int64_t T, int64_t batch, int64_t Hq, int64_t Hk, int64_t d) {
   if (T < 1 || batch < 1 || Hk < 1 || Hq < Hk || Hq % Hk != 0 || (d != 64 && d != 128)) return -1;
-  return paged_workspace(paged_tile_rows(T, batch, Hq / Hk, d), d).bytes;
+  return paged_workspace(paged_tile_rows(T, batch, Hq / Hk), d).bytes;
 }
 
 mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_t ldq, const mxq_paged_kv* cache,
@@ -1057,7 +1056,7 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
   DeviceInfo dev;
   if ((st = current_device(&dev)) != MXQ_OK) return st;
 
-  const int tile_rows = paged_tile_rows(T, batch->batch, Hq / Hk, d);
+  const int tile_rows = paged_tile_rows(T, batch->batch, Hq / Hk);
   const PagedWorkspace ws = paged_workspace(tile_rows, d);
   auto* base = static_cast<uint8_t*>(workspace);
   mxq::PagedParams p = {};
@@ -1085,16 +1084,9 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
   p.v_scale = cache->v_scale;
   const bool fp8 = cache->fmt == MXQ_KV_FP8_E4M3;
-  if (tile_rows == mxq::kChunkRows) {
-    if (d == 128)
-      return fp8 ? launch_paged_chunk<128, true>(dev, cache, p, stream)
-                 : launch_paged_chunk<128, false>(dev, cache, p, stream);
-    return fp8 ? launch_paged_chunk<64, true>(dev, cache, p, stream)
-               : launch_paged_chunk<64, false>(dev, cache, p, stream);
-  }
   if (d == 128)
-    return fp8 ? launch_paged_few<128, true>(dev, cache, p, stream) : launch_paged_few<128, false>(dev, cache, p, stream);
-  return fp8 ? launch_paged_few<64, true>(dev, cache, p, stream) : launch_paged_few<64, false>(dev, cache, p, stream);
+    return fp8 ? launch_paged<128, true>(dev, cache, p, stream) : launch_paged<128, false>(dev, cache, p, stream);
+  return fp8 ? launch_paged<64, true>(dev, cache, p, stream) : launch_paged<64, false>(dev, cache, p, stream);
 }
 
 mxq_status mxq_selftest_wait_timeout(mxq_stream_t stream) {
