@@ -1046,6 +1046,8 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
   if (st != MXQ_OK) return st;
   if (!q_bf16 || !out_bf16 || !workspace) return MXQ_ERR_INVALID_ARG;
   if (!(scale >= 0.f) || !std::isfinite(scale) || window < 0 || (window > 0 && !causal)) return MXQ_ERR_INVALID_ARG;
+  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2)) return MXQ_ERR_INVALID_ARG;
   const int64_t d = cache->d, Hk = cache->heads;
   if (d != 64 && d != 128) return MXQ_ERR_UNSUPPORTED;
   if (T < 1 || Hq < 1 || Hq % Hk != 0 || T * Hq > (int64_t(1) << 30) || T > (int64_t(1) << 30)) return MXQ_ERR_SHAPE;
@@ -1081,7 +1083,7 @@ mxq_status mxq_attention_paged(const void* q_bf16, int64_t T, int64_t Hq, int64_
   p.causal = causal != 0;
   p.window = static_cast<int>(window);
   p.tile_rows = tile_rows;
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * cache->k_scale * 1.4426950408889634);
+  p.scale_log2 = mxq::nonzero_scale(scale_log2);
   p.v_scale = cache->v_scale;
   const bool fp8 = cache->fmt == MXQ_KV_FP8_E4M3;
   if (d == 128)

@@ -572,7 +572,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           tc_fence_after();
           float s[128];
           auto load = [&](int c) { tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c])); };
-          if (kFp8 && k == 0) scale *= q_scale[(units & 1) * kChunkRows + t * kChunkHalf + r];
+          if (kFp8 && k == 0) scale = nonzero_scale(scale * q_scale[(units & 1) * kChunkRows + t * kChunkHalf + r]);
           auto mask = [&](int c, uint32_t there) {
             // bit i of on: key 32 c + i is attended
             const int lo = min(max(kr.x - key0 - 32 * c, 0), 32), hi = min(max(kr.y - key0 - 32 * c, 0), 32);

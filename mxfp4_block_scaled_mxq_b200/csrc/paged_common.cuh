@@ -47,6 +47,10 @@ struct PagedParams {
   float v_scale;
 };
 
+// A score's scale, held off zero (NaN stays): a masked score of -inf must not become NaN.  2^-126 times
+// a score below 2^100 is zero to 2^-26.
+__device__ __host__ __forceinline__ float nonzero_scale(float x) { return x < 0x1p-126f ? 0x1p-126f : x; }
+
 // One sequence: its rows of Q, its length, clamped to what Q and the block table hold.
 struct Sequence {
   int64_t q0;

@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int e = min(static_cast<int>(__float_as_uint(big) >> 23) - 127, 126);
         const bool fits = e >= -126 && big != INFINITY;
         const float down = fits ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
-        const float up = fits ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : p.scale_log2;
+        const float up =
+            fits ? nonzero_scale(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23)) : p.scale_log2;
 #pragma unroll
         for (int s = 0; s < kKs; ++s) {
           const uint32_t w[2] = {raw[s].x, raw[s].y};

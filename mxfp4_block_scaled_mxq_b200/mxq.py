@@ -728,6 +728,8 @@ def attention_paged(q: torch.Tensor, Hq: int, cache: PagedKV, batch: PagedBatch,
         workspace = attention_paged_workspace(T, b.batch, Hq, a.heads, d, q.device)
     else:
         _here(workspace, cur, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: expected a contiguous tensor")
     o = _out_heads(out, q, cur, "out")
     mxq_attention_paged(q.data_ptr(), T, Hq, q.stride(0), a, b, causal, window, d ** -0.5 if scale is None else scale,
                         workspace, workspace.numel() * workspace.element_size(), o.data_ptr(), o.stride(0), stream)

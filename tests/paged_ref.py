@@ -34,10 +34,11 @@ def norm_rope(x, heads, weight, table, positions, eps, row=False, pairs=False):
 def assert_rounded(got, want, mag, scale=1.0):
     """got (BF16, or E4M3 with its scale) is `want` rounded once from an FP32 computation.
 
-    FP32: the sum of squares is off by at most (16 terms a lane x 3 heads a lane + 16 of the tree
-    and the warps) x 2^-24 relative, half of that after the square root; root, division, two
-    products and the rotation's three operations add 8 x 2^-24: under 2^-17 of the pair's
-    magnitude, rotated by |cos|, |sin| <= 1.  Then half a step of the result's type (BF16 2^-8
+    FP32: the sum of squares is off by at most 64 x 2^-24 relative (a term passes through 6 roundings
+    in its lane's head, one for each of up to 33 heads of the lane, and 9 in the tree over lanes and
+    warps), half of that after the square root; the root (2 units in the last place), two products
+    and the rotation's three operations add 9 x 2^-24: under 2^-17 of the pair's magnitude,
+    rotated by |cos|, |sin| <= 1.  Then half a step of the result's type (BF16 2^-8
     relative; E4M3 2^-4 relative, 2^-10 absolute below its normal range)."""
     want, mag = want / scale, mag / scale
     g = got.double()

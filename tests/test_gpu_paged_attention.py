@@ -284,3 +284,111 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("q_lens", [[1, 2], [20, 3]])
+@pytest.mark.parametrize("Hq,Hk,d", [(1024, 1024, 64), (512, 512, 128), (128, 1, 128), (160, 1, 64), (512, 2, 128),
+                                     (1000, 1, 64)])
+def test_many_heads(Hq, Hk, d, q_lens, fp8):
+    """As many key heads as fit, groups of 128 heads (a row tile's half is one token) and larger."""
+    check(make(q_lens, [q_lens[0] + 70, q_lens[1] + 9], Hq, Hk, d, 16, fp8, seed=Hk))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_short_chunks(fp8):
+    """More sequences of many rows than the kernel weighs at once."""
+    q = [17 + i % 5 for i in range(900)]
+    q[7] = q[500] = q[501] = 0
+    check(make(q, [n + (i * 13) % 41 for i, n in enumerate(q)], 2, 2, 64, 8, fp8, seed=20, max_pages=8))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [2, 150])
+def test_a_row_of_nan_stays_alone(n, fp8):
+    """The other rows are held to the formula: rows of a tile raise their maxima together, so the
+    exponents that the weights are rounded at (any between the maximum and 2^8 of it are right)
+    may depend on the neighbours, the error bound does not."""
+    s = make([n, n], [300, 200], 8, 2, 128, 16, fp8, seed=21)
+    want, mags, owned = ref.attention(s["q"], 8, s["k_cache"], s["v_cache"], s["cu_q"], s["kv_len"], s["block_table"],
+                                      k_scale=s["k_scale"], v_scale=s["v_scale"])
+    s["q"][1, 128:256] = float("nan")
+    s["q"][n, 5] = float("inf")
+    out = call(s)
+    assert torch.isnan(out[1, 128:256]).all() and torch.isnan(out[n, :128]).all()
+    out[1, 128:256], out[n, :128] = want[1, 128:256].to(out.dtype), want[n, :128].to(out.dtype)
+    ref.assert_attention(out, want, mags, owned)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,kv", [(3, 100), (2, 6000), (200, 300), (150, 3000)])
+def test_attended_nan_is_seen(n, kv, fp8):
+    """A key or a value that is NaN: every row that attends it is NaN (a value: in its column)."""
+    for which, cols in (("k_cache", slice(0, 64)), ("v_cache", slice(9, 10))):
+        s = make([n], [kv], 2, 1, 64, 16, fp8, seed=22)
+        pos = kv - n + 1
+        cache = s[which].view(torch.uint8) if fp8 else s[which]
+        cache[int(s["block_table"][0, pos // 16]), pos % 16, 0, 9] = 0x7F if fp8 else float("nan")
+        out = call(s).reshape(n, 2, 64)
+        assert torch.isnan(out[1:, :, cols]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [2, 150])
+def test_scale_of_zero_averages(n, fp8):
+    check(make([n, 1], [400, 77], 8, 2, 128, 16, fp8, seed=23), scale=0.0)
+
+
+@pytest.mark.parametrize("n", [2, 150])
+def test_workspace_contents_do_not_matter(n):
+    s = make([n, 1], [4000, 77], 8, 2, 128, 16, seed=24)
+    want = call(s)
+    ws = mxq.attention_paged_workspace(n + 1, 2, 8, 2, 128, "cuda")
+    for fill in (0xFF, 0x00, 0x3C):
+        ws.fill_(fill)
+        assert torch.equal(call(s, workspace=ws), want)
+    with pytest.raises(mxq.MxqError):
+        call(s, workspace=ws[:-256])
+    with pytest.raises(ValueError, match="workspace"):
+        call(s, workspace=ws[:1].expand(ws.numel()))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page", [8, 24, 64, 256])
+@pytest.mark.parametrize("q_lens", [[2, 1, 1], [150, 129, 40]])
+def test_missing_pages_of_every_size(q_lens, page, fp8):
+    """Pages that are missing at the start, inside and at the end of a sequence, in tiles that hold
+    other pages and in tiles without any; the memory of a page that is there but unused is NaN."""
+    s = make(q_lens, [700, 1100, 333], 8, 2, 128, page, fp8, seed=25)
+    n = [-(-k // page) for k in (700, 1100, 333)]
+    for b, entries in enumerate(([0, n[0] // 2], [1, n[1] - 1], [0])):
+        for e in entries:
+            s["block_table"][b, e] = -1 if b else s["k_cache"].shape[0] + e
+    s["block_table"][1, n[1] // 3:n[1] // 2] = -1
+    check(s)
+    check(s, causal=False)
+    check(s, window=200)
+
+
+@pytest.mark.parametrize("page", [8, 64])
+@pytest.mark.parametrize("n", [3, 150])
+def test_garbage_behind_a_window_of_an_e4m3_cache(n, page):
+    """NaN bytes at every position that no row's window reaches."""
+    s = make([n, 1], [600, 300], 4, 2, 128, page, True, seed=26)
+    window = 77
+    clean = call(s, window=window)
+    for b, rows in enumerate((n, 1)):
+        L = int(s["kv_len"][b])
+        for j in range(L - rows - window + 1):
+            for c in (s["k_cache"], s["v_cache"]):
+                c.view(torch.uint8)[int(s["block_table"][b, j // page]), j % page] = 0x7F
+    out = call(s, window=window)
+    assert torch.isfinite(out).all() and torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_long_chunk_among_idle_sequences(fp8):
+    """The kernel is chosen by the mean number of rows; either is right for any lengths."""
+    q = [0] * 120
+    q[50], q[51], q[119] = 300, 1, 7
+    check(make(q, [n + 50 for n in q], 8, 2, 128, 16, fp8, seed=27))

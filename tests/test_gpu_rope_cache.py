@@ -309,3 +309,78 @@ def test_streams_and_graphs(T):
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+@pytest.mark.parametrize("row", [False, True])
+@pytest.mark.parametrize("Hq,Hk,d", [(512, 512, 128), (256, 40, 256), (1024, 3, 64), (455, 455, 144)])
+def test_rows_wider_than_a_block_holds(Hq, Hk, d, row, pairs):
+    """Rows of up to 2^16 values a side are divided over blocks, by heads or (one norm over the
+    row) by operands; in the append queries, keys and values may lie in one block or not."""
+    T = 5
+    q, k, v = _x(T, Hq * d, 80), _x(T, Hk * d, 81), _x(T, Hk * d, 82)
+    qw, kw = _w(Hq * d if row else d, 83), _w(Hk * d if row else d, 84)
+    table = mxq.rope_table(50, d)
+    span, style = (mxq.MXQ_NORM_ROW if row else mxq.MXQ_NORM_HEAD), mxq.MXQ_ROPE_PAIRS if pairs else mxq.MXQ_ROPE_HALVES
+    batch, pages, places = _batch([3, 2], [30, 9], 8, 5)
+    pg, slot, pos = (torch.tensor(z, device="cuda") for z in zip(*places))
+    want_q = ref.norm_rope(q, Hq, qw, table, pos, 1e-6, row, pairs)
+    want_k = ref.norm_rope(k, Hk, kw, table, pos, 1e-6, row, pairs)
+    qo, ko = mxq.qk_norm_rope(q, k, Hq, Hk, qw, kw, 1e-6, span, table, pos.to(torch.int32), style)
+    ref.assert_rounded(qo, *want_q)
+    ref.assert_rounded(ko, *want_k)
+    for queries in (q, None):
+        cache = _cache(pages, 8, Hk, d, False)
+        got = mxq.kv_append(k, v, cache, batch, kw, 1e-6, span, table, style, queries, qw if queries is not None else None)
+        if queries is not None:
+            ref.assert_rounded(got, *want_q)
+        ref.assert_rounded(cache.k[pg, slot].reshape(T, -1), *want_k)
+        assert torch.equal(cache.v[pg, slot].reshape(T, -1), v)
+
+
+def test_more_tokens_than_a_block_looks_up_at_once():
+    """A block takes every so-many-th token and looks 32 up at a time: several such rounds."""
+    T, d, page = 40003, 64, 16
+    q, k, v = _x(T, 2 * d, 85), _x(T, d, 86), _x(T, d, 87)
+    w, table = _w(d, 88), mxq.rope_table(T, d)
+    lens = [T - 40 * 700, *[40] * 700]
+    batch, pages, places = _batch(lens, lens, page, 6)
+    pg, slot, pos = (torch.tensor(z, device="cuda") for z in zip(*places))
+    qo, ko = mxq.qk_norm_rope(q, k, 2, 1, w, w, table=table, positions=pos.to(torch.int32))
+    want_q, want_k = ref.norm_rope(q, 2, w, table, pos, 1e-6), ref.norm_rope(k, 1, w, table, pos, 1e-6)
+    ref.assert_rounded(qo, *want_q)
+    ref.assert_rounded(ko, *want_k)
+    cache = mxq.paged_kv(pages, page, 1, d)
+    assert torch.equal(mxq.kv_append(k, v, cache, batch, w, table=table, q=q, q_weight=w), qo)
+    assert torch.equal(cache.k[pg, slot].reshape(T, -1), ko) and torch.equal(cache.v[pg, slot].reshape(T, -1), v)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_values_that_are_not_finite_stay_in_their_head(bad):
+    """An infinity or NaN spoils its own head's norm; every other head is as without it."""
+    T, H, d = 4, 6, 128
+    q, k = _x(T, H * d, 89), _x(T, H * d, 90)
+    w, table = _w(d, 91), mxq.rope_table(T, d)
+    want_q, want_k = mxq.qk_norm_rope(q, k, H, H, w, w, table=table)
+    q[2, 3 * d + 7] = bad
+    qo, ko = mxq.qk_norm_rope(q, k, H, H, w, w, table=table)
+    assert torch.isnan(qo[2, 3 * d + 7]) and torch.equal(ko, want_k)
+    qo[2, 3 * d:4 * d] = want_q[2, 3 * d:4 * d]
+    assert torch.equal(qo, want_q)
+
+
+def test_e4m3_append_at_the_ends_of_the_type():
+    """Values and keys beyond the type's range saturate, NaN stays NaN, the smallest round to even."""
+    d, page = 64, 8
+    x = torch.zeros(6, d, device="cuda")
+    x[0], x[1], x[2], x[3] = 1e6, -1e6, float("nan"), float("inf")
+    x[4, :4] = torch.tensor([2.0 ** -10, 3 * 2.0 ** -10, 2.0 ** -9, -2.0 ** -11])
+    x[5] = torch.linspace(-460, 460, d)
+    x = x.to(torch.bfloat16)
+    cache = mxq.PagedKV(*(torch.zeros(1, page, 1, d, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2)))
+    z = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    mxq.kv_append(x, x, cache, mxq.PagedBatch(z, z[1:], torch.zeros(1, 1, dtype=torch.int32, device="cuda")))
+    want = x.float().clamp(-448, 448).to(torch.float8_e4m3fn)
+    for c in (cache.k, cache.v):
+        got = c[0, :6, 0].float()
+        assert torch.equal(torch.isnan(got), torch.isnan(x)) and torch.equal(torch.nan_to_num(got), torch.nan_to_num(want.float()))

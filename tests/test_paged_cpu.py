@@ -118,7 +118,7 @@ def test_append_refusals(L, want, kw):
 
 @pytest.mark.parametrize("want,kw", [
     (INV, dict(q=None)), (INV, dict(out=None)), (INV, dict(ws=None)), (INV, dict(wsb=100)), (ALIGN, dict(ws=FAKE + 128)),
-    (INV, dict(scale=float("nan"))), (INV, dict(window=-1)), (INV, dict(window=5, causal=0)),
+    (INV, dict(scale=float("nan"))), (INV, dict(scale=3e38)), (INV, dict(window=-1)), (INV, dict(window=5, causal=0)),
     (SHAPE, dict(window=(1 << 30) + 1)), (SHAPE, dict(Hq=7, ldq=896, ldo=896)), (SHAPE, dict(Hq=0)), (SHAPE, dict(T=0)),
     (SHAPE, dict(T=1 << 28)), (ALIGN, dict(ldo=1000)), (ALIGN, dict(ldq=1028)), (ALIGN, dict(out=FAKE + 8))])
 def test_attention_refusals(L, want, kw):
