@@ -581,8 +581,8 @@ mxq_status launch_paged_chunk(const DeviceInfo& dev, const mxq_paged_kv* c, mxq:
   mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(p.workers)), dim3(S::kThreads), S::kSmemBytes,
                                    stream, tq, tk, tv, p);
   if (st != MXQ_OK) return st;
-  return launch_dependent(mxq::paged_join_many_kernel<D, mxq::kChunkRows>,
-                          dim3(static_cast<unsigned>(p.workers), mxq::kChunkRows / 8), dim3(2 * D), 0, stream, p);
+  return launch_dependent(mxq::paged_join_many_kernel<D, mxq::kChunkRows, kPagedMaxCtas>,
+                          dim3(static_cast<unsigned>(p.workers), 16), dim3(2 * D), 0, stream, p);
 }
 
 template <int D, bool kFp8>

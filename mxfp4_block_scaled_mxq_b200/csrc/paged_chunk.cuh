@@ -39,12 +39,16 @@ constexpr int kChunkSoftWarps = 8;
 constexpr int kChunkProducer = 8, kChunkMma = 9, kChunkConv = 12;  // warps
 constexpr int kChunkConvWarps = 4;
 constexpr int kChunkMasks = 8;  // tiles whose page masks are kept: more than the rings are ahead
-constexpr int kChunkMinTiles = 2;
+constexpr int kChunkMinPlaces = 2;
 constexpr int kChunkEarly = 6;  // of a tile's eight 16-key steps: P V begins when these are there
 
 template <int D, bool kFp8>
 struct ChunkShape {
   static constexpr int kThreads = kFp8 ? 512 : 384;
+  // What a unit costs beside its key tiles, in key tiles.  With 0, 1, 2, 3, 4, 6: chunks of 500 to
+  // 2048 tokens behind up to 8192 (BF16, 32 / 8 heads) 290, 274, 267, 261, 259, 265 us; a 6001-token prompt
+  // (E4M3, 40 / 8 heads), whose first units are short, 575, 522, 479, 441, 437, 445 us.
+  static constexpr int kUnitCost = kFp8 ? 4 : 3;
   // registers a thread: at launch, softmax warps, the other warps
   static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
   static constexpr int kSoftRegs = kFp8 ? 168 : 216;
@@ -195,7 +199,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
   }
   griddep_launch_dependents();
   griddep_wait();
-  const Share sh = find_share<kChunkKeys, S::kThreads, 1, kChunkMinTiles, false>(p, scratch);
+  const Share sh = find_share<kChunkKeys, S::kThreads, 1, kChunkMinPlaces, S::kUnitCost, false>(p, scratch);
   if (tid == 0) p.part_units[blockIdx.x] = make_int4(0, 0, 0, 0);  // nothing to join, also after a timeout
   tc_fence_before();
   __syncthreads();
@@ -208,8 +212,8 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
     if (warp == kChunkProducer) {
       // ------------------------------------------------------------------ TMA producer
       Unit u = sh.u;
-      int tile = sh.tile;
-      int64_t left = sh.count, at = sh.begin;
+      int offset = sh.offset;
+      int64_t left = sh.count, unit_at = sh.begin - sh.offset;
       const int nbox = kChunkKeys / p.page_box, box_shift = 31 - __clz(p.page_box);
       // rings: 0 K, 1 V (as copied)
       constexpr int kRing1 = kFp8 ? S::kRawSlots : S::kVSlots;
@@ -221,7 +225,10 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
       bool ok = true;
       int batch_at = 0, batch_b = -1, entries = -1;  // block-table entries [batch_at, +32) of sequence batch_b
       while (ok && left > 0) {
-        const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
+        const int places = static_cast<int>(min(left, static_cast<int64_t>(S::kUnitCost + u.nt - offset)));
+        const int tile = max(offset - S::kUnitCost, 0), n = max(offset + places - S::kUnitCost, 0) - tile;
+        left -= places;
+        if (n == 0) break;  // the share ends before the unit's first key tile
         ok = __all_sync(0xffffffffu, mbar_wait(&unit_empty[units & 1], ((units >> 1) & 1) ^ 1));
         if (!ok) break;
         if (lane == 0) {
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           c.whole = tile == 0 && n == u.nt;
           c.slot = tile == 0 ? 1 : 0;
           mbar_arrive(&unit_full[units & 1]);
-          if (left == n) p.part_units[blockIdx.x] = part_unit(sh, u, at, tile == 0 && n < u.nt);
+          if (left == 0) p.part_units[blockIdx.x] = part_unit(sh, u, unit_at + S::kUnitCost, tile == 0 && n < u.nt);
         }
         ok = __all_sync(0xffffffffu, mbar_wait(q_empty, (units & 1) ^ 1));
         if (!ok) break;
@@ -301,9 +308,8 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           if (!ok) break;
         }
         if (!ok) break;
-        left -= n;
-        at += n;
-        tile = 0;
+        unit_at += S::kUnitCost + u.nt;
+        offset = 0;
         if (left > 0) next_unit<kChunkKeys, false>(p, u);
       }
       if (ok && __all_sync(0xffffffffu, mbar_wait(&unit_empty[units & 1], ((units >> 1) & 1) ^ 1)) && lane == 0) {

@@ -8,8 +8,8 @@
 //
 // Work.  The query heads of one key head share its keys, so a row is (token, head of the group)
 // and a unit is (sequence, key head, row tile) with the key tiles its rows reach.  All units'
-// key tiles in a line, every worker (a CTA, or a warp in the few-row kernel) takes an equal,
-// contiguous share of it: the load is even whatever the lengths, nothing is planned on the host,
+// key tiles (and, in the many-row kernel, some places for what a unit costs beside them) in a line,
+// every worker (a CTA, or a warp in the few-row kernel) takes an equal, contiguous share of it: the load is even whatever the lengths, nothing is planned on the host,
 // and only the first and the last segment of a share can be a part of a unit.  Such a part goes
 // to the workspace as an unnormalised FP32 accumulator with its row maxima and sums (two
 // slots per worker, so the workspace does not grow with the lengths), and the joining kernel
@@ -105,13 +105,13 @@ __device__ __forceinline__ void set_unit(const PagedParams& p, Unit& u) {
   u.nt = max(1, (r.y + kKeys - 1) / kKeys - u.kt0);
 }
 
-template <int kKeys>
-__device__ __forceinline__ int unit_tiles(const PagedParams& p, const Sequence& s, int rt) {
+template <int kKeys, int kUnitCost>
+__device__ __forceinline__ int unit_weight(const PagedParams& p, const Sequence& s, int rt) {
   Unit u;
   u.rt = rt;
   u.s = s;
   set_unit<kKeys>(p, u);
-  return u.nt;
+  return kUnitCost + u.nt;
 }
 
 // The next unit in the line (row tiles within key heads within sequences).
@@ -133,11 +133,12 @@ __device__ __forceinline__ void next_unit(const PagedParams& p, Unit& u) {
   set_unit<kKeys>(p, u);
 }
 
-// A worker's share of the line: where it begins, and how many key tiles it has.
+// A worker's share of the line: the places [begin, begin + count).  A unit has kUnitCost places for
+// what is spent on it once (nobody's work when a border falls among them), then one per key tile.
 struct Share {
   Unit u;
-  int tile;              // first key tile within the unit
-  int64_t begin, count;  // key tiles: the first one's place in the line, how many
+  int offset;  // of the first place within the unit
+  int64_t begin, count;
   int64_t total;         // the line's length
   int shares;            // into which it is divided
   int index;             // which of them this is
@@ -155,9 +156,9 @@ struct ShareScratch {
 // The share of this thread's worker: the CTA has kWorkers, one for each of its first kWorkers
 // warps (or one for all of them).  Called by all kThreads threads.  Sequences are weighed in
 // parallel, by a warp each when there are few of them (a long chunk has many row tiles), by a
-// thread each otherwise.  A share has at least about kMinTiles key tiles: fewer workers take part in
-// a small call.
-template <int kKeys, int kThreads, int kWorkers, int kMinTiles, bool kPerHead>
+// thread each otherwise.  A share has at least about kMinPlaces: fewer workers take part in a small
+// call.
+template <int kKeys, int kThreads, int kWorkers, int kMinPlaces, int kUnitCost, bool kPerHead>
 __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& sc) {
   constexpr int kWarps = kThreads / 32;
   static_assert(kWarps <= 32 && kWorkers <= kMaxWorkers && kWorkers <= kWarps, "scratch");
@@ -170,7 +171,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
       const Sequence s = load_sequence(p, b);
       const int tiles = row_tiles(p, s);
       for (int rt = by_warp ? lane : 0; rt < tiles; rt += by_warp ? 32 : 1)
-        w += unit_tiles<kKeys>(p, s, rt);
+        w += unit_weight<kKeys, kUnitCost>(p, s, rt);
       if (!kPerHead) w *= p.Hk;
     }
     if (by_warp) {
@@ -193,7 +194,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
     for (int i = 0; i < kWarps; ++i) total += sc.warp_sum[i];
   }
   const int64_t shares =
-      min(static_cast<int64_t>(kPerHead ? p.workers / p.Hk : p.workers), (total + kMinTiles - 1) / kMinTiles);
+      min(static_cast<int64_t>(kPerHead ? p.workers / p.Hk : p.workers), (total + kMinPlaces - 1) / kMinPlaces);
   if (tid < kWorkers) {
     const int g = blockIdx.x * kWorkers + tid;
     const int64_t c = kPerHead ? g / p.Hk : g;
@@ -238,7 +239,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
   sh.index = sc.index[worker];
   sh.total = total;
   sh.shares = static_cast<int>(shares);
-  sh.tile = 0;
+  sh.offset = 0;
   sh.u.b = sc.b[worker];
   if (sh.count > 0) {
     sh.u.s = load_sequence(p, sh.u.b);
@@ -253,7 +254,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
     // the row tile: 32 at a time, each warp for itself
     const int tiles = row_tiles(p, sh.u.s);
     for (int rt0 = 0;; rt0 += 32) {
-      const int w = rt0 + lane < tiles ? unit_tiles<kKeys>(p, sh.u.s, rt0 + lane) : 0;
+      const int w = rt0 + lane < tiles ? unit_weight<kKeys, kUnitCost>(p, sh.u.s, rt0 + lane) : 0;
       int incl = w;
       for (int m = 1; m < 32; m <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, incl, m);
@@ -263,7 +264,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
       if (hit || rt0 + 32 >= tiles) {
         const int l = hit ? __ffs(hit) - 1 : 0;
         sh.u.rt = rt0 + l;
-        sh.tile = static_cast<int>(rest - __shfl_sync(0xffffffffu, incl - w, l));
+        sh.offset = static_cast<int>(rest - __shfl_sync(0xffffffffu, incl - w, l));
         break;
       }
       rest -= __shfl_sync(0xffffffffu, incl, 31);
@@ -273,7 +274,7 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
   return sh;
 }
 
-// The share that has the key tile at place x of the line.
+// The share that has place x of the line.
 __device__ __forceinline__ int owner(const Share& sh, int64_t x) {
   return static_cast<int>(((x + 1) * sh.shares - 1) / sh.total);
 }
@@ -286,7 +287,7 @@ __device__ __forceinline__ int64_t row_offset(const PagedParams& p, int64_t q0, 
 }
 
 // What a worker leaves for the joining kernel: parts 0 unless it began the unit and did not
-// finish it.  `at`: the place in the line of its first tile in the unit.
+// finish it.  `at`: the place in the line of the unit's first key tile.
 __device__ __forceinline__ int4 part_unit(const Share& sh, const Unit& u, int64_t at, bool begun_only) {
   const int parts = begun_only ? owner(sh, at + u.nt - 1) - sh.index + 1 : 0;
   return make_int4(static_cast<int>(u.s.q0), u.rt, u.rows, u.hk * 4096 + parts);
@@ -393,38 +394,71 @@ __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p
   }
 }
 
-// The same for the unit that worker blockIdx.x began, many rows: a block has 8 rows and all
-// groups of four columns; parts are [d / 4][row][4], the layout in which the thread per row that
-// wrote them stored consecutively.
-template <int D, int kRows>
+// The same for the unit that worker blockIdx.x began, many rows: a block has 8 rows at a time and
+// all groups of four columns; parts are [d / 4][row][4], the layout in which the thread per row that
+// wrote them stored consecutively.  A warp finds the factors of a row's parts, a lane each, while
+// the first values are on their way.
+template <int D, int kRows, int kMaxParts>
 __global__ void __launch_bounds__(2 * D) paged_join_many_kernel(const PagedParams p) {
+  constexpr int kWarps = 2 * D / 32, kAhead = 4;
+  __shared__ float s_f[kMaxParts][8], s_inv[8];
   griddep_wait();
-  const int c = blockIdx.x;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, group = threadIdx.x >> 3;
   const int4 un = p.part_units[c];
   const int parts = un.w & 4095;
-  const int r = blockIdx.y * 8 + (threadIdx.x & 7), group = threadIdx.x >> 3;
-  if (parts == 0 || r >= un.z) return;
+  if (parts == 0) return;
   auto slot = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)); };
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) m = max_or_nan(m, p.part_ml[slot(i) * kRows + r].x);
-  const float base = m == -INFINITY ? 0.f : m;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const float2 ml = p.part_ml[slot(i) * kRows + r];
-    const float f = exp2f(ml.x - base);
-    l = fmaf(ml.y, f, l);
-    const float4 v = reinterpret_cast<const float4*>(p.part_o)[(slot(i) * (D / 4) + group) * kRows + r];
-    acc.x = fmaf(v.x, f, acc.x);
-    acc.y = fmaf(v.y, f, acc.y);
-    acc.z = fmaf(v.z, f, acc.z);
-    acc.w = fmaf(v.w, f, acc.w);
+  for (int r0 = blockIdx.y * 8; r0 < un.z; r0 += 8 * gridDim.y) {
+    const int r = r0 + (threadIdx.x & 7);  // below kRows; from un.z on not kept
+    auto value = [&](int i) {
+      return reinterpret_cast<const float4*>(p.part_o)[(slot(i) * (D / 4) + group) * kRows + r];
+    };
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < parts && r < un.z) ahead[i] = value(i);
+    for (int row = threadIdx.x >> 5; row < min(8, un.z - r0); row += kWarps) {
+      constexpr int kMine = (kMaxParts + 31) / 32;
+      float2 ml[kMine];
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        ml[k] = lane + 32 * k < parts ? p.part_ml[slot(lane + 32 * k) * kRows + r0 + row] : make_float2(-INFINITY, 0.f);
+        m = max_or_nan(m, ml[k].x);
+      }
+      for (int k = 16; k > 0; k >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        const float f = exp2f(ml[k].x - base);
+        l = fmaf(ml[k].y, f, l);
+        if (lane + 32 * k < parts) s_f[lane + 32 * k][row] = f;
+      }
+      for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+      if (lane == 0) s_inv[row] = l == 0.f ? 0.f : p.v_scale / l;
+    }
+    __syncthreads();
+    if (r < un.z) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](int i, const float4& v) {
+        const float f = s_f[i][threadIdx.x & 7];
+        acc.x = fmaf(v.x, f, acc.x);
+        acc.y = fmaf(v.y, f, acc.y);
+        acc.z = fmaf(v.z, f, acc.z);
+        acc.w = fmaf(v.w, f, acc.w);
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i < parts) add(i, ahead[i]);
+#pragma unroll 8
+      for (int i = kAhead; i < parts; ++i) add(i, value(i));
+      const float inv = s_inv[threadIdx.x & 7];
+      uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + 4 * group;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+    __syncthreads();
   }
-  const float inv = l == 0.f ? 0.f : p.v_scale / l;
-  uint16_t* dst = p.out + row_offset<D>(p, un.x, un.w >> 12, un.y * p.tile_rows + r, p.ldo) + 4 * group;
-  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
 }  // namespace mxq

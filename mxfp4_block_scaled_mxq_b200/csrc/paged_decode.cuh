@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   griddep_launch_dependents();
   griddep_wait();
-  const Share sh = find_share<kKeys, kDecThreads, kDecWarps, kDecMinTiles, true>(p, scratch);  // has the block's barriers
+  const Share sh = find_share<kKeys, kDecThreads, kDecWarps, kDecMinTiles, 0, true>(p, scratch);  // has the block's barriers
   const int worker = blockIdx.x * kDecWarps + warp;
   if (lane == 0) p.part_units[worker] = make_int4(0, 0, 0, 0);
   if (sh.count == 0) return;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     return (key >> box_shift) * p.page_box * S::kRowBytes + (key & (p.page_box - 1)) * S::kBoxRowBytes;
   };
   Unit lu = sh.u;
-  int ltile = sh.tile;
+  int ltile = sh.offset;
   int64_t lleft = sh.count;
   int batch_at = 0, batch_b = -1, entries = -1;  // block-table entries [batch_at, +32) of sequence batch_b
   uint32_t boxes[kDecStages] = {};               // per stage: boxes whose page is there
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     v_off[mt] = key_offset(16 * mt + (lane & 7) + ((lane >> 4) << 3));
   }
   Unit u = sh.u;
-  int tile = sh.tile;
+  int tile = sh.offset;
   int64_t left = sh.count, at = sh.begin;
   int st = 0;
   uint32_t phase = 0;
