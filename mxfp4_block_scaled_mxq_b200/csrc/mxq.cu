@@ -540,8 +540,7 @@ mxq_status launch_paged_decode(const DeviceInfo& dev, const mxq_paged_kv* c, mxq
                                    stream, tk, tv, p);
   if (st != MXQ_OK) return st;
   return launch_dependent(mxq::paged_join_few_kernel<D, mxq::kDecWarps>,
-                          dim3(static_cast<unsigned>(ctas), 8), dim3(256), 0,
-                          stream, p);
+                          dim3(static_cast<unsigned>(ctas), mxq::kDecWarps), dim3(256), 0, stream, p);
 }
 
 // Q as (128-byte piece, piece, head, token): a box is one piece of the G heads of whole tokens.

@@ -297,9 +297,10 @@ __device__ __forceinline__ int4 part_unit(const Share& sh, const Unit& u, int64_
 __device__ __forceinline__ float max_or_nan(float a, float b) { return a != a || a >= b ? a : b; }
 
 // Joins the parts of the units that the kWorkers workers of CTA blockIdx.x began: the worker's last
-// slot, then the first slots of the workers of the next shares of its head.  gridDim.y blocks take
-// the pairs of a worker and a row in turn: a warp each where the unit has up to kJoinWarpParts
-// parts, else a block (a unit that spans the whole machine has over a thousand).
+// slot, then the first slots of the workers of the next shares of its head.  gridDim.y = kWorkers
+// blocks take the pairs of a worker and a row in turn: a warp each where the unit has up to
+// kJoinWarpParts parts, else a block (a unit that spans the whole machine has over a thousand; 20000
+// keys of one key head, eight rows: 24 us with its rows in different blocks, 128 in one).
 constexpr int kJoinWarpParts = 32;
 
 template <int D, int kWorkers>
@@ -314,13 +315,22 @@ __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p
   __syncthreads();
   // Units of few parts: a warp each, D / 32 columns a lane.
   const int pairs = kWorkers * p.tile_rows;  // of a worker and a row
-  for (int q = blockIdx.y * 8 + (threadIdx.x >> 5); q < pairs; q += 8 * gridDim.y) {
-    constexpr int kCols = D / 32;
+  for (int q = blockIdx.y * 8 + (threadIdx.x >> 5); q < pairs; q += 8 * kWorkers) {
+    constexpr int kCols = D / 32, kAhead = 4;
     const int w = q % kWorkers, r = q / kWorkers, c = blockIdx.x * kWorkers + w;
     const int4 un = s_units[w];
     const int parts = un.w & 4095;
     if (parts > 0 && parts <= kJoinWarpParts && r < un.z) {
       auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i * p.Hk)) * p.tile_rows + r; };
+      auto value = [&](int i, float (&v)[kCols]) {
+        const float* o = p.part_o + row_of(i) * D + lane * kCols;
+        if constexpr (kCols == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
+        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+      };
+      float ahead[kAhead][kCols];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i < parts) value(i, ahead[i]);
       const float2 mine = lane < parts ? p.part_ml[row_of(lane)] : make_float2(-INFINITY, 0.f);
       float m = mine.x;
       for (int k = 16; k > 0; k >>= 1) m = max_or_nan(m, __shfl_xor_sync(0xffffffffu, m, k));
@@ -328,15 +338,19 @@ __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p
       float l = mine.y * f;
       for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
       float acc[kCols] = {};
-#pragma unroll 8
-      for (int i = 0; i < parts; ++i) {
+      auto add = [&](int i, const float (&v)[kCols]) {
         const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float* o = p.part_o + row_of(i) * D + lane * kCols;
-        float v[kCols];
-        if constexpr (kCols == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
-        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
 #pragma unroll
         for (int k = 0; k < kCols; ++k) acc[k] = fmaf(v[k], fi, acc[k]);
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i < parts) add(i, ahead[i]);
+#pragma unroll 4
+      for (int i = kAhead; i < parts; ++i) {
+        float v[kCols];
+        value(i, v);
+        add(i, v);
       }
       const float inv = l == 0.f ? 0.f : p.v_scale / l;
       uint32_t h[kCols / 2];
@@ -347,9 +361,10 @@ __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p
       else *reinterpret_cast<uint32_t*>(dst) = h[0];
     }
   }
-  // The others: the whole block, slices of the parts side by side.
-  for (int q = blockIdx.y; q < pairs; q += gridDim.y) {
-    const int w = q % kWorkers, r = q / kWorkers, c = blockIdx.x * kWorkers + w;
+  // The others: the whole block, slices of the parts side by side; the kWorkers blocks take the
+  // rows of a unit, and the units of a row, in turn.
+  for (int r = 0; r < p.tile_rows; ++r) {
+    const int w = (blockIdx.y + r) % kWorkers, c = blockIdx.x * kWorkers + w;
     const int4 un = s_units[w];
     const int parts = un.w & 4095;
     if (parts <= kJoinWarpParts || r >= un.z) continue;
