@@ -302,7 +302,7 @@ __device__ __forceinline__ int4 part_unit(const Share& sh, const Unit& u, int64_
 __device__ __forceinline__ float max_or_nan(float a, float b) { return a != a || a >= b ? a : b; }
 
 // Joins the parts of the units that the kWorkers workers of CTA blockIdx.x began: the worker's last
-// slot, then the first slots of the workers of the next shares of its head.  gridDim.y = kWorkers
+// slot, then the first slots of the workers of the next shares of its head.  gridDim.y
 // blocks take the pairs of a worker and a row in turn: a warp each where the unit has up to
 // kJoinWarpParts parts, else a block (a unit that spans the whole machine has over a thousand; 20000
 // keys of one key head, eight rows: 24 us with its rows in different blocks, 128 in one).
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p
   __syncthreads();
   // Units of few parts: a warp each, D / 32 columns a lane.
   const int pairs = kWorkers * p.tile_rows;  // of a worker and a row
-  for (int q = blockIdx.y * 8 + (threadIdx.x >> 5); q < pairs; q += 8 * kWorkers) {
+  for (int q = blockIdx.y * 8 + (threadIdx.x >> 5); q < pairs; q += 8 * gridDim.y) {
     constexpr int kCols = D / 32, kAhead = 4;
     const int w = q % kWorkers, r = q / kWorkers, c = blockIdx.x * kWorkers + w;
     const int4 un = s_units[w];
@@ -366,10 +366,10 @@ __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p
       else *reinterpret_cast<uint32_t*>(dst) = h[0];
     }
   }
-  // The others: the whole block, slices of the parts side by side; the kWorkers blocks take the
-  // rows of a unit, and the units of a row, in turn.
-  for (int r = 0; r < p.tile_rows; ++r) {
-    const int w = (blockIdx.y + r) % kWorkers, c = blockIdx.x * kWorkers + w;
+  // The others: the whole block, slices of the parts side by side; the rows of a unit, and the
+  // units of a row, are in different blocks.
+  for (int q = blockIdx.y; q < pairs; q += gridDim.y) {
+    const int r = q / kWorkers, w = (q + r) % kWorkers, c = blockIdx.x * kWorkers + w;
     const int4 un = s_units[w];
     const int parts = un.w & 4095;
     if (parts <= kJoinWarpParts || r >= un.z) continue;
