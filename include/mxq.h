@@ -400,8 +400,8 @@ MXQ_API mxq_status mxq_attention_mxfp4(const void* q_codes, const void* q_sf, co
  * strides multiples of 16 bytes and at least d; page_size a multiple of 8; heads * d <= 2^16.
  *
  * mxq_paged_batch -- `batch` sequences (up to 2^20): the rows [cu_q[b], cu_q[b + 1]) of Q, K, V are sequence b's
- * new tokens (cu_q[0] = 0, non-decreasing; none is fine; rows from cu_q[batch] on belong to no
- * sequence), kv_len[b] its length with them, and block_table[b][i] the page of its positions
+ * new tokens (cu_q[0] = 0, non-decreasing, cu_q[batch] <= T; none is fine; rows from cu_q[batch] on
+ * belong to no sequence), kv_len[b] its length with them, and block_table[b][i] the page of its positions
  * [i * page_size, (i + 1) * page_size).  New token i of n has position kv_len[b] - n + i.  All
  * device int32; max_pages * page_size <= 2^30.  Table entries outside [0, num_pages) are
  * pages that are missing: nothing is stored there, and their positions are not attended.
@@ -472,9 +472,12 @@ MXQ_API mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* c
  * with window > 0 (causal only) also j > position - window.  A row that attends nothing is 0;
  * rows of no sequence are not written.  Lengths are clamped to the block table's capacity.
  * Softmax statistics and sums are FP32; the weights are rounded to the product's operand type
- * (BF16; FP16 in the few-row kernel of an E4M3 cache), the result once to BF16.  Cached
- * positions that no row of a sequence attends may hold anything (NaN, Inf); a non-finite value
- * of a key attended by some row may reach other rows of the same sequence.
+ * (BF16; FP16 with an E4M3 cache, whose queries are exact down to 2^-14 of their row's largest
+ * value and off by at most 2^-17 of it below), the result once to BF16.  Cached positions that no
+ * row of a sequence attends may hold anything (NaN, Inf); a non-finite value of a key attended by
+ * some row may reach other rows of the same sequence.  How the work is divided, and with it the
+ * rounding of a row, depends on the lengths of all sequences of the call; the same lengths give
+ * the same bits.
  *
  * q_bf16 [T][ldq], out_bf16 [T][ldo] with Hq heads of d, Hq a multiple of the cache's heads, T * Hq <= 2^30;
  * d 64 or 128 (else MXQ_ERR_UNSUPPORTED).  workspace: device, 256-byte aligned, at least

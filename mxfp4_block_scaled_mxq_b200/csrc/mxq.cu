@@ -508,10 +508,10 @@ PagedWorkspace paged_workspace(int tile_rows, int64_t d) {
 
 // Which kernel, by the rows that share a key head: the few-row one streams the cache once per row tile of
 // 8 or 16 rows, the other computes 256 whether they are there or not.  24 sequences of 4000 keys,
-// 8 key heads, d = 128, BF16 (E4M3): 16 rows 85 (65) us against some 98 (103) us, 32 rows 100 (93)
-// against 98 (103), 48 rows 136 (125) against 100 (104); four sequences of 1000 keys: 32 rows 28 (25)
-// against 18 (20).  By the mean over the sequences, since the lengths are on the device: every
-// kernel is right for any.
+// 8 key heads, d = 128, BF16 (E4M3): 16 rows 84 (64) us against 92 (103) us, 32 rows 99 (92) against 93
+// (103); four sequences of 1000 keys: 16 rows 26 (22) us against 18 (21), 32 rows 26 (23) against 18
+// (21).  By the mean over the sequences, since the lengths are on the device: every kernel is right
+// for any.
 int paged_tile_rows(int64_t T, int64_t batch, int64_t G) {
   const int64_t rows = (T * G + batch - 1) / batch;
   if (rows <= 8) return 8;

@@ -9,11 +9,12 @@
 // Work.  The query heads of one key head share its keys, so a row is (token, head of the group)
 // and a unit is (sequence, key head, row tile) with the key tiles its rows reach.  All units'
 // key tiles (and, in the many-row kernel, some places for what a unit costs beside them) in a line,
-// every worker (a CTA, or a warp in the few-row kernel) takes an equal, contiguous share of it: the load is even whatever the lengths, nothing is planned on the host,
-// and only the first and the last segment of a share can be a part of a unit.  Such a part goes
-// to the workspace as an unnormalised FP32 accumulator with its row maxima and sums (two
-// slots per worker, so the workspace does not grow with the lengths), and the joining kernel
-// adds the parts of each unit in the order of the keys.
+// every worker (a CTA, or a warp in the few-row kernel) takes an equal, contiguous share of it: the
+// load is even whatever the lengths, nothing is planned on the host, and only the first and the
+// last segment of a share can be a part of a unit.  Such a part goes to the workspace as an
+// unnormalised FP32 accumulator with its row maxima and sums (two slots per worker, so the
+// workspace does not grow with the lengths), and the joining kernel adds the parts of each unit in
+// an order that the lengths fix.
 //
 // kPerHead (the few-row kernel, which has over a thousand workers): the line is one key head's, and
 // workers g, g + 1, ... take the same share of heads g mod Hk, so that the heads of a token are
