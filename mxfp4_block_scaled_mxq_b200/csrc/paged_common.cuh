@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(256) paged_join_few_kernel(const PagedParams p
   __shared__ float s_m[8], s_l[kSlices];
   __shared__ float4 s_o[kSlices][kGroups];
   __shared__ int4 s_units[kWorkers];
+  griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, group = threadIdx.x % kGroups, slice = threadIdx.x / kGroups;
   if (threadIdx.x < kWorkers) s_units[threadIdx.x] = p.part_units[blockIdx.x * kWorkers + threadIdx.x];
@@ -423,6 +424,7 @@ template <int D, int kRows, int kMaxParts>
 __global__ void __launch_bounds__(2 * D) paged_join_many_kernel(const PagedParams p) {
   constexpr int kWarps = 2 * D / 32, kAhead = 4;
   __shared__ float s_f[kMaxParts][8], s_inv[8];
+  griddep_launch_dependents();
   griddep_wait();
   const int c = blockIdx.x, lane = threadIdx.x & 31, group = threadIdx.x >> 3;
   const int4 un = p.part_units[c];
