@@ -196,11 +196,13 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
   }
   int64_t shares =
       min(static_cast<int64_t>(kPerHead ? p.workers / p.Hk : p.workers), (total + kMinPlaces - 1) / kMinPlaces);
-  // One key tile more in every share costs what some 16 parts more cost in the join: a few long sequences
+  // One key tile more in every share costs what some 16 parts more cost in the join: a few long units
   // have about four times the square root of their tiles in parts (20000 keys of one key head:
   // 20 us, with all workers 25; 100000: 33, 38; with the factor 2: 25 and 45).
-  if (kPerHead)
-    shares = min(shares, static_cast<int64_t>(4.f * sqrtf(static_cast<float>(total) * static_cast<float>(p.batch))) + 1);
+  if (kPerHead) {
+    const float units = fmaxf(static_cast<float>(p.batch), static_cast<float>(p.T * p.G / p.tile_rows));
+    shares = min(shares, static_cast<int64_t>(4.f * sqrtf(static_cast<float>(total) * units)) + 1);
+  }
   if (tid < kWorkers) {
     const int g = blockIdx.x * kWorkers + tid;
     const int64_t c = kPerHead ? g / p.Hk : g;
