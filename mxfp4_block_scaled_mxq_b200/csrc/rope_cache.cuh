@@ -16,9 +16,9 @@
 // warps read a token's heads from there.  A lane owns 16 values of one head, two 16-byte chunks
 // chosen so that both members of every rotated pair are its own (`rot / 2` apart for halves), as
 // u[8] and v[8], the pairs' first and second members, on which the packed FP32 operations work.
-// cos and sin then depend on the lane alone and are read once per token, the rotation needs no
-// shuffle, and a head's sum of squares takes log2(lanes per head) of them.  Instructions are the
-// next bound: some 110 per 16 values.
+// cos and sin then depend on the lane alone, the rotation needs no shuffle, and a head's sum of
+// squares takes log2(lanes per head) of them.  Instructions are the next bound: some 110 per 16
+// values.
 #pragma once
 
 #include "gemm_common.cuh"
@@ -26,9 +26,11 @@
 
 namespace mxq {
 
-// Threads that compute (and a warp that copies).  Four CTAs per SM at 64 registers: at 32760 x 80
-// heads with a norm over the row 278 us, against 310 with two of 320 threads at 80 registers,
-// and 387 with two of 480.
+// Threads that compute (and a warp that copies).  Four CTAs per SM at 64 registers, with nothing kept
+// on the stack: the cosines stay in registers over a token's heads, the sines are read from shared
+// memory again for each (both in registers: 278 us for 32760 x 80 heads with a norm over the row, a
+// third of the loads being of spilled registers; so 255 us; both read again 260).  Fewer threads with
+// more registers are slower (three CTAs at 80 registers 311 us with all in registers).
 constexpr int kRopeMaxThreads = 224;
 constexpr int kRopeCtas = 4;
 constexpr int kRopeMaxStages = 16;
@@ -159,7 +161,8 @@ template <int kCache, bool kPairs>
 __global__ void __launch_bounds__(kRopeMaxThreads + 32, kRopeCtas) rope_cache_kernel(const RopeParams p, const AppendParams a) {
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[kRopeMaxStages], empty[kRopeMaxStages], sums;
-  __shared__ int64_t s_token[kRopeMaxStages], s_slot[kRopeMaxStages];  // token -1: no more
+  __shared__ int64_t s_slot[kRopeMaxStages];
+  __shared__ int s_token[kRopeMaxStages];  // -1: no more
   static_assert(kRopeMaxThreads <= 16 * 32, "a lane per warp's sum");
   __shared__ float s_sum[2][2][kRopeMaxThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31;
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kRopeMaxThreads + 32, kRopeCtas) rope_cache_ke
         issued |= 1u << stage;
         issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
         if (lane == 0) {
-          s_token[stage] = tt;
+          s_token[stage] = static_cast<int>(tt);
           s_slot[stage] = tslot;
           mbar_arrive_expect_tx(&full[stage], p.stage_bytes_of(h1 - h0));
         }
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(kRopeMaxThreads + 32, kRopeCtas) rope_cache_ke
   uint32_t phase = 0;
   for (;;) {
     if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) break;
-    const int64_t t = s_token[stage];
+    const int t = s_token[stage];
     if (t < 0) break;
     const int64_t slot = s_slot[stage];
     const uint8_t* src = ring + stage * p.stage_bytes;
@@ -317,23 +320,18 @@ __global__ void __launch_bounds__(kRopeMaxThreads + 32, kRopeCtas) rope_cache_ke
       parity ^= 1;  // the next token's sums go elsewhere: these may still be read
     }
 
-    float cs[8], sn[8];
+    float cs[8];
     if (rot0 || rot1) {
       const float4* row = reinterpret_cast<const float4*>(src + (h1 - h0) * p.d * 2);
-      const int half = p.rot >> 3;  // the sines, in float4
       // pairs: four of a chunk; halves: eight of the lane
       const int a0 = kPairs ? c0 : 2 * j, a1 = kPairs ? c1 : 2 * j + 1;
       if (rot0) {
         *reinterpret_cast<float4*>(cs) = row[a0];
-        *reinterpret_cast<float4*>(sn) = row[half + a0];
       }
       if (rot1) {
         *reinterpret_cast<float4*>(cs + 4) = row[a1];
-        *reinterpret_cast<float4*>(sn + 4) = row[half + a1];
       }
     }
-    uint16_t* const q_row = p.q.out + t * p.q.ldo;
-    uint16_t* const k_row = p.k.out + t * p.k.ldo;
     // A warp's groups take the same number of steps (the shuffles below are warp-wide).
     for (int base = h0; base < h1; base += groups) {
       const int h = base + g0;
@@ -368,6 +366,11 @@ __global__ void __launch_bounds__(kRopeMaxThreads + 32, kRopeCtas) rope_cache_ke
             set_pair(v, i, __fmul2_rn(__fmul2_rn(pair_of(v, i), r2), pair_of(wv, i)));
           }
         }
+        // (read here: the registers do not hold them over the heads)
+        const float4* sines = reinterpret_cast<const float4*>(src + (h1 - h0) * p.d * 2) + (p.rot >> 3);
+        float sn[8];
+        if (rot0) *reinterpret_cast<float4*>(sn) = sines[kPairs ? c0 : 2 * j];
+        if (rot1) *reinterpret_cast<float4*>(sn + 4) = sines[kPairs ? c1 : 2 * j + 1];
         auto rotate = [&](int i) {
           const float2 c = pair_of(cs, i), sp = pair_of(sn, i), sm = make_float2(-sp.x, -sp.y);
           const float2 x = pair_of(u, i), y = pair_of(v, i);
@@ -384,7 +387,8 @@ __global__ void __launch_bounds__(kRopeMaxThreads + 32, kRopeCtas) rope_cache_ke
         }
       }
       if (kCache == 0 || is_q) {
-        uint4* out = reinterpret_cast<uint4*>((is_q ? q_row : k_row) + hh * p.d);
+        const RopeOperand& o = is_q ? p.q : p.k;
+        uint4* out = reinterpret_cast<uint4*>(o.out + t * o.ldo + hh * p.d);
         out[c0] = pack_bf16<kPairs>(u, v, 0);
         out[c1] = pack_bf16<kPairs>(u, v, 1);
       } else if (slot >= 0) {
