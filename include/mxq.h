@@ -441,7 +441,7 @@ typedef struct {
  * mxq_qk_norm_rope -- q_out = bf16(norm and rotation of Q), k_out likewise, one launch.
  * q_bf16 [T][ldq] with Hq heads of d, k_bf16 [T][ldk] with Hk heads; either may be NULL (its
  * other arguments are then ignored).  positions: device int32 [T], or NULL for 0, 1, 2, ...;
- * a row whose position is outside [0, table_rows) is not written.  Outputs may be the inputs
+ * with a table, a row whose position is outside [0, table_rows) is not written.  Outputs may be the inputs
  * (same pointer and row stride); otherwise they do not overlap them.  Leading dimensions: at
  * least heads * d, multiples of 8; 16-byte aligned pointers; heads * d <= 2^16.
  */
@@ -467,7 +467,7 @@ MXQ_API mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* c
 /*
  * mxq_attention_paged -- attention of the new tokens of every sequence over its cached keys and
  * values (the new ones among them), for each query head h with key head h / (Hq / heads):
- *   O = sum_j softmax_j(scale * q . K_j) V_j,  scale >= 0,
+ *   O = sum_j softmax_j(scale * q . K_j) V_j,  scale >= 0 (scale * k_scale within FP32),
  * over the keys j < kv_len of pages that are there; with `causal` also j <= the token's position;
  * with window > 0 (causal only) also j > position - window.  A row that attends nothing is 0;
  * rows of no sequence are not written.  Lengths are clamped to the block table's capacity.

@@ -392,3 +392,23 @@ def test_a_long_chunk_among_idle_sequences(fp8):
     q = [0] * 120
     q[50], q[51], q[119] = 300, 1, 7
     check(make(q, [n + 50 for n in q], 8, 2, 128, 16, fp8, seed=27))
+
+
+@pytest.mark.parametrize("n", [1, 150])
+def test_graphs_with_one_workspace_in_turn(n):
+    """Two captured calls of different lengths share a workspace and replay one after another."""
+    sets = [make([n, n], [3000, 200], 8, 2, 128, 16, seed=28), make([n, n], [n, 5000], 8, 2, 128, 16, True, seed=29)]
+    want = [call(s) for s in sets]
+    ws = mxq.attention_paged_workspace(2 * n, 2, 8, 2, 128, "cuda")
+    outs, graphs = [torch.zeros_like(w) for w in want], []
+    torch.cuda.synchronize()
+    for s, o in zip(sets, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(s, out=o, workspace=ws)
+        graphs.append(g)
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))

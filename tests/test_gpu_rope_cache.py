@@ -384,3 +384,19 @@ def test_e4m3_append_at_the_ends_of_the_type():
     for c in (cache.k, cache.v):
         got = c[0, :6, 0].float()
         assert torch.equal(torch.isnan(got), torch.isnan(x)) and torch.equal(torch.nan_to_num(got), torch.nan_to_num(want.float()))
+
+
+def test_append_with_queries_in_place():
+    """Q, K and V as slices of one projection, the queries rotated where they are."""
+    batch, pages, places = _batch([30, 1], [60, 33], 16, 7)
+    Hq, Hk, d = 8, 2, 128
+    x = _x(31, (Hq + 2 * Hk) * d, 92)
+    before = x.clone()
+    q, k, v = x[:, :Hq * d], x[:, Hq * d:(Hq + Hk) * d], x[:, (Hq + Hk) * d:]
+    qw, kw, table = _w(d, 93), _w(d, 94), mxq.rope_table(64, d)
+    pos = torch.tensor([p for _, _, p in places], device="cuda")
+    want = ref.norm_rope(q, Hq, qw, table, pos, 1e-6)
+    cache = _cache(pages, 16, Hk, d, False)
+    assert mxq.kv_append(k, v, cache, batch, kw, table=table, q=q, q_weight=qw, q_out=q) is q
+    ref.assert_rounded(q, *want)
+    assert torch.equal(x[:, Hq * d:], before[:, Hq * d:])
