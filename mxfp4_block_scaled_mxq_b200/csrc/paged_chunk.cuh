@@ -50,8 +50,10 @@ struct ChunkShape {
   static constexpr int kThreads = kFp8 ? 512 : 384;
   // What a unit costs beside its key tiles, in key tiles.  With 0, 1, 2, 3, 4, 6: chunks of 500 to
   // 2048 tokens behind up to 8192 (BF16, 32 / 8 heads) 290, 274, 267, 261, 259, 265 us; a 6001-token prompt
-  // (E4M3, 40 / 8 heads), whose first units are short, 575, 522, 479, 441, 437, 445 us.
-  static constexpr int kUnitCost = kFp8 ? 4 : 3;
+  // (E4M3, 40 / 8 heads), whose first units are short, 575, 522, 479, 441, 437, 445 us.  d = 64, a
+  // 6000-token prompt, 32 / 8 heads, with 1 to 5: BF16 260, 252, 259, 262, 268 us, E4M3 305, 281, 285, 288,
+  // 293 us (eight of 700 tokens 73, 70, 68, 67, 65 us).
+  static constexpr int kUnitCost = (kFp8 ? 4 : 3) - (D == 64 ? 1 : 0);
   // registers a thread: at launch, softmax warps, the other warps
   static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
   static constexpr int kSoftRegs = kFp8 ? 168 : 216;
