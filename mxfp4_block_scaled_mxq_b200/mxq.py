@@ -545,11 +545,12 @@ def _current(x: torch.Tensor, name: str) -> int:
     return torch.cuda.current_device()
 
 
-def _here(x: torch.Tensor, cur: int, name: str) -> None:
-    if x.get_device() != cur:
+def _here(x: torch.Tensor, dev: int, name: str) -> None:
+    """Refuses x unless it is on device `dev`, the current one or that of the tensors it belongs to."""
+    if x.get_device() != dev:
         if not x.is_cuda:
             raise ValueError(f"{name}: expected a CUDA tensor")
-        _on_current_device(x, name)
+        raise ValueError(f"{name}: tensor on {x.device}, expected one on cuda:{dev}")
 
 
 def _width(x: torch.Tensor, heads: int, d: int, name: str) -> None:
@@ -625,7 +626,7 @@ def paged_kv(pages: int, page_size: int, heads: int, d: int, fmt: int = MXQ_KV_B
 
 class PagedBatch:
     """The sequences of a call: cu_q [batch + 1], kv_len [batch] and block_table [batch][max_pages], int32 on
-    the GPU (see mxq_paged_batch).  Holds the tensors: their contents may change between calls."""
+    one GPU (see mxq_paged_batch).  Holds the tensors: their contents may change between calls."""
 
     __slots__ = ("cu_q", "kv_len", "block_table", "args")
 
@@ -633,7 +634,7 @@ class PagedBatch:
         if block_table.dim() != 2:
             raise ValueError("block_table: expected [batch][max_pages]")
         batch, max_pages = block_table.shape
-        dev = block_table.get_device()
+        dev = cu_q.get_device()  # the others are on it too: a call checks cu_q alone
         self.args = PagedBatchArgs(_int32(cu_q, (batch + 1,), dev, "cu_q"), _int32(kv_len, (batch,), dev, "kv_len"),
                                    _int32(block_table, (batch, max_pages), dev, "block_table"), batch, max_pages)
         self.cu_q, self.kv_len, self.block_table = cu_q, kv_len, block_table
