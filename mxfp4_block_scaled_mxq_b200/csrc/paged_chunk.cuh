@@ -619,7 +619,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           // The weights of scores [64 h, +64), in place, for the maximum m as it is.
           const float2 sc2 = make_float2(scale, scale);
           auto weights = [&](int h) {
-            const float base = m == -INFINITY ? 0.f : -m;
+            const float base = weight_base<kFp8>(m);
             const float2 nb2 = make_float2(base, base);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -629,8 +629,8 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
               s[j + 1] = ex2(x.y);
             }
           };
-          // P rounded to the operand type (BF16: 2^-8 relative at most, FP16: 2^-11), random over the
-          // keys, over columns whose scores have been read: 16 weights, 8 columns.
+          // P rounded to the operand type (BF16: 2^-8 relative at most, FP16: 2^-11, and 2^-32 of the
+          // largest weight), random over the keys, over columns whose scores have been read: 16 weights, 8 columns.
           auto store = [&](int c) {
             uint32_t w[8];
 #pragma unroll
@@ -659,7 +659,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
             weights(0);
             float mx = fmax3_nan(fmax3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]) * scale;
             if (mx == INFINITY) mx = NAN;
-            // raised when it would let P pass 2^8 (and when a score is NaN: then the row's maximum, sum
+            // raised when it would let 2^(t - m) pass 2^8 (and when a score is NaN: then the row's maximum, sum
             // and result are)
             const bool raise = !(mx <= m + 8.f);
             if (__any_sync(0xffffffffu, raise)) {

@@ -52,6 +52,16 @@ struct PagedParams {
 // a score below 2^100 is zero to 2^-26.
 __device__ __host__ __forceinline__ float nonzero_scale(float x) { return x < 0x1p-126f ? 0x1p-126f : x; }
 
+// The weights 2^(t - m) of an E4M3 cache are rounded to FP16: 2^-11 relative, but 2^-25 absolute below its normal
+// range, where small ones vanish from the product and not from the row sum (one strong key over a flat
+// tail loses the tail).  So they are taken as 2^(t - m + 7), in sums and parts alike, which cancels in O / l: the
+// running maximum is at most 8 behind, so that they reach 2^15 (FP16 holds up to 2^16), and a weight is off by
+// 2^-32 of the largest at most.  BF16 has FP32's exponents and needs no shift.
+template <bool kFp8>
+__device__ __forceinline__ float weight_base(float m) {  // added to t
+  return m == -INFINITY ? 0.f : (kFp8 ? 7.f : 0.f) - m;
+}
+
 // One sequence: its rows of Q, its length, clamped to what Q and the block table hold.
 struct Sequence {
   int64_t q0;

@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
           for (int mt = 1; mt < kMt; ++mt) x = fmaxf(x, fmaxf(sc[mt][t][i], sc[mt][t][i + 2]));
           mx[t][i] = x * t_scale[t][i];
-          raise |= !(mx[t][i] <= m[t][i] + 8.f);  // P would pass 2^8
+          raise |= !(mx[t][i] <= m[t][i] + 8.f);  // 2^(t - m) would pass 2^8
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -372,11 +372,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           }
       }
       // P rounded to the cache's operand type (BF16: 2^-8, FP16: 2^-11 relative at most, random over
-      // keys), transposed
+      // keys; FP16 also 2^-32 of the largest weight), transposed
       uint32_t pb[kMt][kNt][2];
 #pragma unroll
       for (int t = 0; t < kNt; ++t) {
-        const float b0 = m[t][0] == -INFINITY ? 0.f : -m[t][0], b1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
+        const float b0 = weight_base<kFp8>(m[t][0]), b1 = weight_base<kFp8>(m[t][1]);
 #pragma unroll
         for (int mt = 0; mt < kMt; ++mt)
 #pragma unroll
