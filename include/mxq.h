@@ -480,7 +480,8 @@ MXQ_API mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* c
  * the same bits.
  *
  * q_bf16 [T][ldq], out_bf16 [T][ldo] with Hq heads of d, Hq a multiple of the cache's heads, T * Hq <= 2^30;
- * d 64 or 128 (else MXQ_ERR_UNSUPPORTED).  workspace: device, 256-byte aligned, at least
+ * d 64 or 128 (else MXQ_ERR_UNSUPPORTED, as with more key heads than eight times the SMs: a partition of
+ * under 128 SMs).  workspace: device, 256-byte aligned, at least
  * mxq_attention_paged_workspace_bytes(T, batch, Hq, heads, d) bytes (-1 for invalid arguments);
  * nothing in it has to be set.  Calls that share a workspace must not overlap.
  */

@@ -494,7 +494,7 @@ struct PagedWorkspace {
 };
 
 constexpr int kPagedMaxCtas = 160;  // at least the SMs of any sm_100 device
-static_assert(kPagedMaxCtas * mxq::kDecWarps < 4096, "a unit's parts are counted in 12 bits");
+static_assert(mxq::dec_workers(kPagedMaxCtas) < 4096, "a unit's parts are counted in 12 bits");
 
 PagedWorkspace paged_workspace(int tile_rows, int64_t d) {
   auto up = [](int64_t v) { return (v + 255) / 256 * 256; };
@@ -524,14 +524,15 @@ template <int D, bool kFp8, int kNt>
 mxq_status launch_paged_decode(const DeviceInfo& dev, const mxq_paged_kv* c, mxq::PagedParams p,
                                cudaStream_t stream) {
   using S = mxq::DecShape<D, kFp8>;
+  const int ctas = std::min(dev.sm_count, kPagedMaxCtas);
+  if (!mxq::dec_covers(ctas, p.Hk)) return MXQ_ERR_UNSUPPORTED;
   auto kernel = mxq::paged_decode_kernel<D, kFp8, kNt>;
   static PerDevice setup;
   if (!setup.ensure(dev.index, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmemBytes) == cudaSuccess;
       }))
     return MXQ_ERR_CUDA;
-  const int ctas = std::min(dev.sm_count, kPagedMaxCtas);
-  p.workers = ctas * mxq::kDecWarps;
+  p.workers = mxq::dec_workers(ctas);
   p.page_box = gcd(p.page_size, S::kKeys);
   CUtensorMap tk, tv;
   if (!make_tmap_cache(&tk, c, c->k, p.page_box, true) || !make_tmap_cache(&tv, c, c->v, p.page_box, true))

@@ -35,6 +35,11 @@ constexpr int kDecStages = 3;  // of each warp
 constexpr int kDecStageBytes = 8192;
 constexpr int kDecMinTiles = 2;  // 777 keys x 8 heads: 13.6 us, with 4 14.7, with 1 20.3, with 8 16.1
 
+// Workers of `ctas` CTAs, and whether every key head has one: shares are of one head's line, so with fewer
+// workers than heads nobody would have any (1024 heads of 64 on a partition of fewer than 128 SMs).
+__host__ __device__ constexpr int dec_workers(int ctas) { return ctas * kDecWarps; }
+__host__ __device__ constexpr bool dec_covers(int ctas, int heads) { return dec_workers(ctas) >= heads; }
+
 template <int D, bool kFp8>
 struct DecShape {
   static constexpr int kRowBytes = D * (kFp8 ? 1 : 2);
