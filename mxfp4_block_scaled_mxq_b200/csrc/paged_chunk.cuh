@@ -17,9 +17,10 @@
 //                other half's softmax; P V begins when three quarters of P are there.
 //   warps 12..15 E4M3 cache only: V tiles to FP16 (which holds E4M3 exactly), Q to two E4M3 terms.
 // E4M3 cache: K is used as it is, by kind::f8f6f4 at twice the rate, with every Q row scaled by a
-// power of two and split into two E4M3 terms (four bits each of BF16's eight, so the split is
-// exact down to 2^-14 of the row's largest value and off by 2^-17 of that at most below); P and V are
-// FP16.  BF16 cache: everything is BF16.
+// power of two and split into two E4M3 terms: four bits each of BF16's eight, in steps of 2^-9 at least where
+// the row's largest value is in [2^7, 2^8).  So the split is exact down to 2^-9 of the largest value and off by
+// 2^-17 of that at most below; rows whose largest is under 2^-119 count as zeros.  P and V are FP16.
+// BF16 cache: everything is BF16.
 // The scores and the accumulator of both halves fill TMEM, so a half's next scores wait for its
 // P V: its softmax and its products alternate, and their latencies bound the kernel.  Per key tile
 // 1.83 us with both halves (d = 128, BF16: 1.36 PFLOP/s; E4M3 2.17 us) against 1.63 (1.84) with one, and

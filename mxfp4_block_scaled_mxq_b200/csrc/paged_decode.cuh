@@ -17,8 +17,8 @@
 //
 // BF16 cache: operands by ldmatrix from the 128-byte-swizzled tiles, P rounded to BF16.
 // E4M3 cache: K and V are converted to FP16, which holds E4M3 exactly; Q is scaled per row by
-// a power of two into FP16 (11 bits, exact for BF16's 8 down to 2^-14 of the row's largest
-// value) and P is rounded to FP16.  The order of the head dimension in the first product and of the
+// a power of two into FP16 (11 bits: exact for BF16's 8 down to 2^-17 of the row's largest value, off by
+// 2^-25 of that at most below) and P is rounded to FP16.  The order of the head dimension in the first product and of the
 // output columns in the second is free, so each lane takes contiguous bytes of K rows (16) and
 // V rows (D / 8) and no byte is shuffled across lanes.
 #pragma once

@@ -1,5 +1,6 @@
 """Paged attention (mxq_attention_paged) at the ends of its numbers' ranges, against the formula in 64 bits: one key
-over a flat tail of far smaller weights, in the few-row and the many-row kernel."""
+over a flat tail of far smaller weights, and queries with an outlier channel, in the few-row and the
+many-row kernel."""
 
 import math
 
@@ -56,3 +57,50 @@ def test_a_strong_key_over_a_flat_tail(fp8, n, d, L, at):
     err = (out.double() - want).abs()
     tol = weights + (2.0 ** -8 + 2.0 ** -14) * want
     assert (err <= tol).all(), (float((err / tol).max()), float((err / want).max()))
+
+
+def _outlier_channel(n, d, low, ratio, seed):
+    """An E4M3 cache and queries whose channel 7 is `ratio` times the others, with keys small in it.  `low`: the
+    least magnitude of the other channels, whose largest is below 4 (0: a normal's values)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    L, page = 300, 16
+    pages = -(-L // page)
+    k, v = torch.randn(2, pages, page, 2, d, generator=g, device="cuda").unbind(0)
+    k[..., 7] /= ratio
+    k, v = ((c / 0.02).clamp(-448, 448).to(torch.float8_e4m3fn) for c in (k, v))
+    q = torch.randn(n, 2 * d, generator=g, device="cuda")
+    if low:
+        q = q.sign() * (low + q.abs()).clamp(max=4 - 2.0 ** -6)
+    for h in range(2):
+        q[:, h * d + 7] = ratio * (1 + 0.9 * torch.rand(n, generator=g, device="cuda"))
+    return dict(q=q.to(torch.bfloat16), Hq=2, k_cache=k, v_cache=v, k_scale=0.02, v_scale=0.02,
+                cu_q=torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                kv_len=torch.tensor([L], dtype=torch.int32, device="cuda"),
+                block_table=torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None])
+
+
+def _against_formula(s, query_error):
+    """query_error(row's largest): how far a query value may be off.  A score is then off by that x scale x sum |K_j|
+    over the channels, at most D over the keys; a weight and the sum of the weights change by e^D each."""
+    out = call(s)
+    want, mags, _ = ref.attention(s["q"], 2, s["k_cache"], s["v_cache"], s["cu_q"], s["kv_len"], s["block_table"],
+                                  k_scale=0.02, v_scale=0.02)
+    d = s["q"].shape[1] // 2
+    big = s["q"].double().reshape(-1, 2, d).abs().amax(2)
+    keys = (s["k_cache"].float().double() * 0.02).abs().sum(3).amax((0, 1))
+    far = torch.expm1(2 * query_error(big) * keys * d ** -0.5).repeat_interleave(d, 1)
+    # the weights' and the result's rounding and FP32 scores as in ref.assert_attention
+    tol = (2.0 ** -8 + 2.0 ** -9 + far) * mags + 2.0 ** -8 * want.abs()
+    err = (out.double() - want).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,bits,off", [(3, 17, 25), (14, 17, 25), (40, 9, 17), (300, 9, 17)])
+def test_queries_with_an_outlier_channel(n, bits, off, d):
+    """An E4M3 cache: queries are exact down to 2^-bits of their row's largest value (few rows 2^-17, many 2^-9) and
+    off by 2^-off of it at most below."""
+    exact = 2.0 ** (bits - 1)  # 1 / 1.9 of it is above 2^-bits
+    _against_formula(_outlier_channel(n, d, 1.0, exact, n), lambda big: 0.0 * big)
+    for ratio in (2.0 ** 9, 2.0 ** 11):
+        _against_formula(_outlier_channel(n, d, 0.0, ratio, n + 1), lambda big: 2.0 ** -off * big)
