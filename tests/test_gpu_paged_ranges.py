@@ -10,7 +10,7 @@ import torch
 import paged_ref as ref
 from mxfp4_block_scaled_mxq_b200 import build, mxq
 from parity import assert_status_clean
-from test_gpu_paged_attention import call
+from test_gpu_paged_attention import call, make
 
 pytestmark = pytest.mark.gpu
 
@@ -104,3 +104,49 @@ def test_queries_with_an_outlier_channel(n, bits, off, d):
     _against_formula(_outlier_channel(n, d, 1.0, exact, n), lambda big: 0.0 * big)
     for ratio in (2.0 ** 9, 2.0 ** 11):
         _against_formula(_outlier_channel(n, d, 0.0, ratio, n + 1), lambda big: 2.0 ** -off * big)
+
+
+def _time(f, reps):
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(2 * reps)]
+    for a, b in zip(events[::2], events[1::2]):
+        a.record()
+        f()
+        b.record()
+    torch.cuda.synchronize()
+    return sorted(a.elapsed_time(b) for a, b in zip(events[::2], events[1::2]))[reps // 2]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n", [20, 130])
+def test_rows_that_are_not_there_cost_no_time(n, fp8):
+    """Rows behind the last sequence that hold NaN, in the same tile as rows that are there: they change neither the
+    result nor, by more than a twentieth, the time."""
+    pad, Hk = 256 - n, 8
+    s = make([n], [60000], Hk, Hk, 128, 16, fp8, pad=pad, seed=30)
+    other = {**s, "q": s["q"].clone()}
+    s["q"][n:], other["q"][n:] = 0.0, float("nan")
+    ws = mxq.attention_paged_workspace(n + pad, 1, Hk, Hk, 128, "cuda")
+    outs = [torch.zeros_like(s["q"]) for _ in range(2)]
+    ratios = []
+    for _ in range(5):  # clocks move: the least of some pairs taken in turn
+        zero, nan = (_time(lambda: call(x, out=o, workspace=ws), 30) for x, o in zip((s, other), outs))
+        ratios.append(nan / zero)
+    assert torch.equal(outs[0][:n], outs[1][:n])
+    assert min(ratios) < 1.05, ratios
+
+
+@pytest.mark.parametrize("kv", [60, 900])
+@pytest.mark.parametrize("n", [3, 14, 150])
+def test_an_infinite_key(n, kv):
+    """A BF16 key with an infinity in one channel: rows whose query is positive there are NaN, rows whose query
+    is negative do not attend it, whichever tile or part it is in."""
+    for pos in (0, kv // 2, kv - 1):
+        s = make([n], [kv], 2, 2, 64, 16, seed=31)
+        s["k_cache"][int(s["block_table"][0, pos // 16]), pos % 16, 0, 9] = float("inf")
+        out = call(s, causal=False)
+        want, mags, _ = ref.attention(s["q"], 2, s["k_cache"], s["v_cache"], s["cu_q"], s["kv_len"], s["block_table"],
+                                      causal=False)
+        up = s["q"][:, 9] > 0
+        assert torch.isnan(out[up, :64]).all() and up.any() and not up.all()
+        out[up, :64], want[up, :64], mags[up, :64] = 0.0, 0.0, 1.0
+        ref.assert_attention(out, want, mags, torch.ones(n, dtype=torch.bool, device="cuda"))
