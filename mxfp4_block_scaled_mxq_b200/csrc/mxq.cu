@@ -432,8 +432,10 @@ mxq_status launch_rope_cache_as(const DeviceInfo& dev, mxq::RopeParams p, const 
   const int k_heads = p.k.heads * (kCache ? 2 : 1);
   const int heads = p.q.heads + k_heads;
   const int table = p.table ? p.rot * 4 : 0;
-  // Heads per block: all of a token's, or as many as leave a CTA room for two tokens; a norm over
-  // the row keeps each operand whole (at most 128 KB: heads * d <= 2^16).
+  // Heads per block: all of a token's, or as many as leave each of four CTAs room for one token; a norm over
+  // the row keeps each operand whole (at most 128 KB: heads * d <= 2^16).  Rows of 28 to 56 KB have one
+  // stage, and the other CTAs' copies run meanwhile (8192 tokens of 64 + 64 + 64 heads of 128 appended, BF16: 141 us,
+  // 0.89 of the measured copy).
   int seg = heads, blocks_y = 1;
   const int fit = std::max(1, (kMaxSmem / 4 - table) / (p.d * 2));
   if (heads > fit) {
@@ -511,7 +513,9 @@ PagedWorkspace paged_workspace(int tile_rows, int64_t d) {
 // 8 key heads, d = 128, BF16 (E4M3): 16 rows 84 (64) us against 92 (103) us, 32 rows 99 (92) against 93
 // (103); four sequences of 1000 keys: 16 rows 26 (22) us against 18 (21), 32 rows 26 (23) against 18
 // (21).  By the mean over the sequences, since the lengths are on the device: every kernel is right
-// for any.
+// for any, but in a mixed call some sequences have the slower one (tokens of 2000 keys beside a chunk behind
+// 2000, 32 / 8 heads, one call against two: 255 + one of 512, few-row kernel, BF16 355 against 332 + 43 us, E4M3
+// 323 against 173 + 52; 63 + one of 2048, many-row kernel, 254 against 94 + 126, 293 against 57 + 145).
 int paged_tile_rows(int64_t T, int64_t batch, int64_t G) {
   const int64_t rows = (T * G + batch - 1) / batch;
   if (rows <= 8) return 8;

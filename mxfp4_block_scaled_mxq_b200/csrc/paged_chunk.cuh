@@ -53,9 +53,11 @@ struct ChunkShape {
   // 2048 tokens behind up to 8192 (BF16, 32 / 8 heads) 290, 274, 267, 261, 259, 265 us; a 6001-token prompt
   // (E4M3, 40 / 8 heads), whose first units are short, 575, 522, 479, 441, 437, 445 us.  d = 64, a
   // 6000-token prompt, 32 / 8 heads, with 1 to 5: BF16 260, 252, 259, 262, 268 us, E4M3 305, 281, 285, 288,
-  // 293 us (eight of 700 tokens 73, 70, 68, 67, 65 us).
+  // 293 us (eight of 700 tokens, 16 / 16 heads: 73, 70, 68, 67, 65 us).
   static constexpr int kUnitCost = (kFp8 ? 4 : 3) - (D == 64 ? 1 : 0);
-  // registers a thread: at launch, softmax warps, the other warps
+  // registers a thread: at launch, softmax warps, the other warps.  Some values of the softmax and of the converter
+  // are kept on the stack for all that (bytes stored / loaded: BF16 96 / 128, d = 64 56 / 76; E4M3 412 / 480, 344 / 412;
+  // 3 % of the L1's cycles in a 6001-token E4M3 prompt).
   static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
   static constexpr int kSoftRegs = kFp8 ? 168 : 216;
   static constexpr int kCtrlRegs = kFp8 ? 88 : 72;

@@ -207,8 +207,9 @@ __device__ __forceinline__ Share find_share(const PagedParams& p, ShareScratch& 
   int64_t shares =
       min(static_cast<int64_t>(kPerHead ? p.workers / p.Hk : p.workers), (total + kMinPlaces - 1) / kMinPlaces);
   // One key tile more in every share costs what some 16 parts more cost in the join: a few long units
-  // have about four times the square root of their tiles in parts (20000 keys of one key head:
-  // 20 us, with all workers 25; 100000: 33, 38; with the factor 2: 25 and 45).
+  // have about four times the square root of their tiles in parts (one token, BF16, 20000 keys of one key head:
+  // 20 to 22 us, with all workers 25; 100000: 33 to 36, 38; with the factor 2: 25 and 45).  The workers that
+  // take part are those of the first CTAs, so these times hold the bandwidth of few SMs as well.
   if (kPerHead) {
     const float units = fmaxf(static_cast<float>(p.batch), static_cast<float>(p.T * p.G / p.tile_rows));
     shares = min(shares, static_cast<int64_t>(4.f * sqrtf(static_cast<float>(total) * units)) + 1);
@@ -318,7 +319,8 @@ __device__ __forceinline__ float max_or_nan(float a, float b) { return a != a ||
 // slot, then the first slots of the workers of the next shares of its head.  gridDim.y
 // blocks take the pairs of a worker and a row in turn: a warp each where the unit has up to
 // kJoinWarpParts parts, else a block (a unit that spans the whole machine has over a thousand; 20000
-// keys of one key head, eight rows: 24 us with its rows in different blocks, 128 in one).
+// keys of one key head, eight rows, parts by all workers: 24 us with its rows in different blocks, 128 in one;
+// 20 to 22 with the parts of find_share).
 constexpr int kJoinWarpParts = 32;
 
 template <int D, int kWorkers>
