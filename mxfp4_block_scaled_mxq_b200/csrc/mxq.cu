@@ -544,7 +544,7 @@ mxq_status launch_paged_decode(const DeviceInfo& dev, const mxq_paged_kv* c, mxq
   mxq_status st = launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), dim3(mxq::kDecThreads), S::kSmemBytes,
                                    stream, tk, tv, p);
   if (st != MXQ_OK) return st;
-  // Few sequences begin in few CTAs, whose units need more blocks (8000 keys of one sequence, 8 key heads:
+  // Few sequences begin in few CTAs, whose units need more blocks (8000 keys of one sequence, 32 / 8 heads:
   // 27 us with 8, 22 with 16); for many, more blocks only take longer to start (64 of 1000 keys: 52, 53).
   const unsigned join_blocks = p.batch <= 8 ? 16 : 8;
   return launch_dependent(mxq::paged_join_few_kernel<D, mxq::kDecWarps>, dim3(static_cast<unsigned>(ctas), join_blocks),
