@@ -471,7 +471,8 @@ MXQ_API mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* c
  * over the keys j < kv_len of pages that are there; with `causal` also j <= the token's position;
  * with window > 0 (causal only) also j > position - window.  A row that attends nothing is 0;
  * rows of no sequence are not written.  Lengths are clamped to the block table's capacity.
- * Softmax statistics and sums are FP32; the weights are rounded to the product's operand type (BF16;
+ * Softmax statistics and sums are FP32 (the tensor core's, which are cut and not rounded, over at most 2^16
+ * keys: 0.03 % of a sum); the weights are rounded to the product's operand type (BF16;
  * FP16 with an E4M3 cache, by 2^-32 of the row's largest weight where that is more), the result once
  * to BF16.  With an E4M3 cache and more than 16 rows per key head the queries are exact down to 2^-9 of their
  * row's largest value and off by at most 2^-17 of it below, and rows whose largest is under 2^-119

@@ -8,7 +8,7 @@
 //                the scores, row sums in FP32; at the end O / l to BF16, or the FP32 part to the
 //                workspace.  (Two threads per row, with an exchange of their maxima, took 364 us
 //                where this took 321: 1560 x 9360 rows x keys, 40 heads.)
-//   warp 8       takes the CTA's share apart into segments of units for the others (through shared
+//   warp 8       takes the CTA's share apart into segments of units, and these into runs, for the others (through shared
 //                memory: carried by every thread, a unit's bounds cost the softmax registers); TMA:
 //                Q of the unit once, then K and V tiles in turn, a box per page (zero fill for pages
 //                that are missing or that no row reaches), into rings.
@@ -44,6 +44,7 @@ constexpr int kChunkProducer = 8, kChunkMma = 9, kChunkConv = 12;  // warps
 constexpr int kChunkConvWarps = 4;
 constexpr int kChunkMasks = 8;  // tiles whose page masks are kept: more than the rings are ahead
 constexpr int kChunkMinPlaces = 2;
+constexpr int kChunkRun = kRunKeys / kChunkKeys;  // tiles
 constexpr int kChunkEarly = 6;  // of a tile's eight 16-key steps: P V begins when these are there
 
 template <int D, bool kFp8>
@@ -56,8 +57,8 @@ struct ChunkShape {
   // 293 us (eight of 700 tokens, 16 / 16 heads: 73, 70, 68, 67, 65 us).
   static constexpr int kUnitCost = (kFp8 ? 4 : 3) - (D == 64 ? 1 : 0);
   // registers a thread: at launch, softmax warps, the other warps.  Some values of the softmax and of the converter
-  // are kept on the stack for all that (bytes stored / loaded: BF16 96 / 128, d = 64 56 / 76; E4M3 412 / 480, 344 / 412;
-  // 3 % of the L1's cycles in a 6001-token E4M3 prompt).
+  // are kept on the stack for all that (bytes stored / loaded: BF16 96 / 128, d = 64 56 / 76; E4M3 400 / 472,
+  // 332 / 404; 3 % of the L1's cycles in a 6001-token E4M3 prompt).
   static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
   static constexpr int kSoftRegs = kFp8 ? 168 : 216;
   static constexpr int kCtrlRegs = kFp8 ? 88 : 72;
@@ -82,13 +83,14 @@ struct ChunkShape {
   static_assert(kSmemBytes <= 232448 - 1024, "shared memory");
 };
 
-// A segment of a unit as the producer hands it on.
+// A segment of a unit, or a run of it, as the producer hands it on.
 struct ChunkUnit {
   int tiles;  // 0: no more
   int key0;   // of the first tile
   int lo, hi, rows, i0, i1, hk;
   Sequence s;
-  int whole, slot;  // all of the unit; else which of the CTA's two slots its part goes to
+  int whole, slot;  // the unit is complete with this; else which of the CTA's two slots its part goes to
+  int joined;       // there is a part of it in the slot already
 };
 
 constexpr uint32_t kChunkTmemCols = 512;
@@ -134,6 +136,28 @@ __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// O <- O x own + before x scale for this thread's row of the accumulator; `before`: its part of the run before,
+// [d / 4][row][4].  Ahead of the unit's output rather than in it: nearly all units have one run, and take one branch.
+template <int D>
+__device__ __forceinline__ void join_accumulator(uint32_t taddr, const float* before, float own, float scale, bool live) {
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t v[16];
+    __syncwarp();
+    tmem_ld16(taddr + 16 * c, v);
+    tmem_ld_wait();
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = __float_as_uint(
+            fmaf(__uint_as_float(v[i]), own, before[((4 * c + i / 4) * kChunkRows) * 4 + i % 4] * scale));
+    }
+    __syncwarp();
+    tmem_st16(taddr + 16 * c, v);
+  }
+  tmem_st_wait();
 }
 
 template <int D, bool kFp8>
@@ -220,7 +244,7 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
     if (warp == kChunkProducer) {
       // ------------------------------------------------------------------ TMA producer
       Unit u = sh.u;
-      int offset = sh.offset;
+      int offset = sh.offset, begun = max(offset - S::kUnitCost, 0);  // the tile at which the CTA began the unit
       int64_t left = sh.count, unit_at = sh.begin - sh.offset;
       const int nbox = kChunkKeys / p.page_box, box_shift = 31 - __clz(p.page_box);
       // rings: 0 K, 1 V (as copied)
@@ -233,9 +257,10 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
       bool ok = true;
       int batch_at = 0, batch_b = -1, entries = -1;  // block-table entries [batch_at, +32) of sequence batch_b
       while (ok && left > 0) {
-        const int places = static_cast<int>(min(left, static_cast<int64_t>(S::kUnitCost + u.nt - offset)));
-        const int tile = max(offset - S::kUnitCost, 0), n = max(offset + places - S::kUnitCost, 0) - tile;
-        left -= places;
+        const int tile = max(offset - S::kUnitCost, 0);
+        const int end = static_cast<int>(min(left + offset, static_cast<int64_t>(S::kUnitCost + min(u.nt, tile + kChunkRun))));
+        const int n = max(end - S::kUnitCost, 0) - tile;
+        left -= end - offset;
         if (n == 0) break;  // the share ends before the unit's first key tile
         ok = __all_sync(0xffffffffu, mbar_wait(&unit_empty[units & 1], ((units >> 1) & 1) ^ 1));
         if (!ok) break;
@@ -250,10 +275,11 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           c.i1 = u.i1;
           c.hk = u.hk;
           c.s = u.s;
-          c.whole = tile == 0 && n == u.nt;
-          c.slot = tile == 0 ? 1 : 0;
+          c.whole = begun == 0 && tile + n == u.nt;
+          c.slot = begun == 0 ? 1 : 0;
+          c.joined = tile > begun;
           mbar_arrive(&unit_full[units & 1]);
-          if (left == 0) p.part_units[blockIdx.x] = part_unit(sh, u, unit_at + S::kUnitCost, tile == 0 && n < u.nt);
+          if (left == 0) p.part_units[blockIdx.x] = part_unit(sh, u, unit_at + S::kUnitCost, begun == 0 && tile + n < u.nt);
         }
         // Q: to L2 while the unit before still has its place (1560 tokens over 9360 keys 324 -> 319 us)
         const int halves = u.rows > half_rows ? 2 : 1;
@@ -323,9 +349,12 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
           if (!ok) break;
         }
         if (!ok) break;
-        unit_at += S::kUnitCost + u.nt;
-        offset = 0;
-        if (left > 0) next_unit<kChunkKeys, false>(p, u);
+        offset = end;
+        if (end == S::kUnitCost + u.nt) {
+          unit_at += end;
+          offset = begun = 0;
+          if (left > 0) next_unit<kChunkKeys, false>(p, u);
+        }
       }
       if (ok && __all_sync(0xffffffffu, mbar_wait(&unit_empty[units & 1], ((units >> 1) & 1) ^ 1)) && lane == 0) {
         chunk_units[units & 1].tiles = 0;
@@ -744,8 +773,13 @@ __global__ void __launch_bounds__((ChunkShape<D, kFp8>::kThreads), 1)
         if (ok) {
           tc_fence_after();
           const bool whole = u.whole != 0;
-          const float inv = l == 0.f ? 0.f : p.v_scale / l;
           const int64_t part_slot = 2 * static_cast<int64_t>(blockIdx.x) + u.slot;
+          if (u.joined) {
+            RunJoin join = {1.f, 0.f};
+            if (live) join = join_run(p.part_ml[part_slot * kChunkRows + row], m, l);
+            join_accumulator<D>(tO, p.part_o + (part_slot * (D / 4) * kChunkRows + row) * 4, join.own, join.before, live);
+          }
+          const float inv = l == 0.f ? 0.f : p.v_scale / l;
           uint16_t* dst = p.out + (u.s.q0 + u.i0 + row_tok) * p.ldo + static_cast<int64_t>(u.hk * p.G + row_head) * D;
           // parts: [four columns][row], so that a warp's stores are consecutive
           float4* part = reinterpret_cast<float4*>(p.part_o) + part_slot * (D / 4) * kChunkRows + row;

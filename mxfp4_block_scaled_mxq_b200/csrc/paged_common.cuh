@@ -62,6 +62,25 @@ __device__ __forceinline__ float weight_base(float m) {  // added to t
   return m == -INFINITY ? 0.f : (kFp8 ? 7.f : 0.f) - m;
 }
 
+// Keys that are added up in one accumulator.  The tensor core's FP32 sums are cut, not rounded: a step of 16
+// keys loses some 1.6e-7 of the sum so far, always toward zero (positive values, 2^20 keys: 0.5 %, 2^22: 2.6 %).
+// So a worker's part of a unit is taken in runs of at most this many keys (0.03 %), each joined to the ones before
+// in the worker's place in the workspace, in rounded FP32.
+constexpr int kRunKeys = 65536;
+
+// What joins a run (m, l, O) to the part before it, of maximum ml.x and sum ml.y: O <- O x own + part x before.
+struct RunJoin {
+  float own, before;
+};
+
+__device__ __forceinline__ RunJoin join_run(float2 ml, float& m, float& l) {
+  const float top = fmaxf(m, ml.x), base = top == -INFINITY ? 0.f : top;
+  const RunJoin j = {exp2f(m - base), exp2f(ml.x - base)};
+  l = fmaf(l, j.own, ml.y * j.before);
+  m = top;
+  return j;
+}
+
 // One sequence: its rows of Q, its length, clamped to what Q and the block table hold.
 struct Sequence {
   int64_t q0;

@@ -205,13 +205,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     v_off[mt] = key_offset(16 * mt + (lane & 7) + ((lane >> 4) << 3));
   }
   Unit u = sh.u;
-  int tile = sh.offset;
+  int tile = sh.offset, begun = tile;  // the tile at which this worker began the unit
   int64_t left = sh.count, at = sh.begin;
   int st = 0;
   uint32_t phase = 0;
   bool ok = true;
   while (ok && left > 0) {
-    const int n = static_cast<int>(min(left, static_cast<int64_t>(u.nt - tile)));
+    const int n = static_cast<int>(min(left, static_cast<int64_t>(min(u.nt - tile, kRunKeys / kKeys))));
     uint32_t qb[kKs][kNt][2];
     float t_scale[kNt][2];
     int klo[kNt][2], khi[kNt][2];  // the keys that rows 8 t + 2 c, + 1 attend
@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (!ok) break;
 
     // O / l to BF16, or this part of the unit to the workspace.
-    const bool whole = tile == 0 && n == u.nt;
-    const int64_t slot = 2 * static_cast<int64_t>(worker) + (tile == 0 ? 1 : 0);
+    const bool whole = begun == 0 && tile + n == u.nt;
+    const int64_t slot = 2 * static_cast<int64_t>(worker) + (begun == 0 ? 1 : 0);
     // columns of o[s][t]: E4M3 r D / 8 + 2 s (accumulators 0, 1) and the next (2, 3); BF16 16 s + r and + 8
 #pragma unroll
     for (int t = 0; t < kNt; ++t) {
@@ -454,6 +454,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 8);
         l[t][i] += __shfl_xor_sync(0xffffffffu, l[t][i], 16);
         const int row = 8 * t + 2 * c + i;
+        if (tile > begun) {
+          if (row < u.rows) {
+            const RunJoin join = join_run(p.part_ml[slot * p.tile_rows + row], m[t][i], l[t][i]);
+            const float* src = p.part_o + (slot * p.tile_rows + row) * D + (kFp8 ? r * (D / 8) : r);
+#pragma unroll
+            for (int s = 0; s < kKs; ++s) {
+              o[s][t][i] = fmaf(o[s][t][i], join.own, src[kFp8 ? 2 * s : 16 * s] * join.before);
+              o[s][t][i + 2] = fmaf(o[s][t][i + 2], join.own, src[kFp8 ? 2 * s + 1 : 16 * s + 8] * join.before);
+            }
+          }
+          __syncwarp();  // a row's maximum and sum are read by eight lanes, one of which writes them below
+        }
         if (whole) {
           const float inv = l[t][i] == 0.f ? 0.f : p.v_scale / l[t][i];
 #pragma unroll
@@ -501,11 +513,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
       }
     }
-    if (lane == 0 && left == n && tile == 0 && n < u.nt) p.part_units[worker] = part_unit(sh, u, at, true);
+    if (lane == 0 && left == n && begun == 0 && tile + n < u.nt) p.part_units[worker] = part_unit(sh, u, at - tile, true);
     left -= n;
     at += n;
-    tile = 0;
-    if (left > 0) next_unit<kKeys, true>(p, u);
+    tile += n;
+    if (tile == u.nt) {
+      tile = begun = 0;
+      if (left > 0) next_unit<kKeys, true>(p, u);
+    }
   }
   if (!ok) {
     // a timeout: wait for the copies in flight

@@ -150,3 +150,48 @@ def test_an_infinite_key(n, kv):
         assert torch.isnan(out[up, :64]).all() and up.any() and not up.all()
         out[up, :64], want[up, :64], mags[up, :64] = 0.0, 0.0, 1.0
         ref.assert_attention(out, want, mags, torch.ones(n, dtype=torch.bool, device="cuda"))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 14, 20])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_sums_over_millions_of_keys(fp8, n, d):
+    """As many sequences as workers, so that each one's 4 x 2^20 keys (one page, four times) are added up in one place:
+    positive values, whose sums only grow.  Four copies of the keys have the result of one."""
+    g = torch.Generator(device="cuda").manual_seed(n + d)
+    page, times = 1 << 20, 4
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    k = torch.randn(1, page, 1, d, generator=g, device="cuda").to(dtype)
+    v = (1 + torch.rand(1, page, 1, d, generator=g, device="cuda")).to(dtype)
+    B = torch.cuda.get_device_properties(0).multi_processor_count * (8 if n <= 16 else 1)
+    q = torch.randn(n, d, generator=g, device="cuda").to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = mxq.PagedBatch(torch.arange(B + 1, **i32) * n, torch.full((B,), times * page, **i32),
+                           torch.zeros(B, times, **i32))
+    out = mxq.attention_paged(q.repeat(B, 1), 1, mxq.PagedKV(k, v), batch, causal=False)
+    want, mags, owned = ref.attention(q, 1, k, v, torch.tensor([0, n], **i32), torch.tensor([page], **i32),
+                                      torch.zeros(1, 1, **i32), causal=False)
+    ref.assert_attention(out, *(x.repeat(B, 1) for x in (want, mags)), owned.repeat(B))
+
+
+@pytest.mark.parametrize("n", [1, 14, 20, 150])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_one_sequence_of_many_millions_of_keys(fp8, n):
+    """A unit in parts by all workers, each long enough to be added up in several runs, with a length that ends
+    inside a page (one page of 2^20 tokens, listed 80 times): key j of the page counts 80 or 79 times."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    page, times, d = 1 << 20, 80, 64
+    L = times * page - 12345
+    dtype = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    k, v = (torch.randn(1, page, 1, d, generator=g, device="cuda").to(dtype) for _ in range(2))
+    q = torch.randn(n, d, generator=g, device="cuda").to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    batch = mxq.PagedBatch(torch.tensor([0, n], **i32), torch.tensor([L], **i32), torch.zeros(1, times, **i32))
+    out = mxq.attention_paged(q, 1, mxq.PagedKV(k, v), batch, causal=False)
+    keys, vals = k[0, :, 0].float().double(), v[0, :, 0].float().double()
+    counts = torch.where(torch.arange(page, device="cuda") < page - 12345, times, times - 1).double()
+    want, mags = torch.empty(2, n, d, dtype=torch.float64, device="cuda").unbind(0)
+    for i in range(0, n, 32):
+        w = torch.softmax(q[i:i + 32].double() @ keys.T * d ** -0.5 + counts.log(), 1)
+        want[i:i + 32], mags[i:i + 32] = w @ vals, w @ vals.abs()
+    ref.assert_attention(out, want, mags, torch.ones(n, dtype=torch.bool, device="cuda"))
