@@ -58,7 +58,7 @@ struct ChunkShape {
   static constexpr int kUnitCost = (kFp8 ? 4 : 3) - (D == 64 ? 1 : 0);
   // registers a thread: at launch, softmax warps, the other warps.  Some values of the softmax and of the converter
   // are kept on the stack for all that (bytes stored / loaded: BF16 96 / 128, d = 64 56 / 76; E4M3 400 / 472,
-  // 332 / 404; 3 % of the L1's cycles in a 6001-token E4M3 prompt).
+  // 332 / 404; 2 to 3 % of the L1's cycles in a 6001-token E4M3 prompt).
   static constexpr int kLaunchRegs = kFp8 ? 128 : 168;
   static constexpr int kSoftRegs = kFp8 ? 168 : 216;
   static constexpr int kCtrlRegs = kFp8 ? 88 : 72;
