@@ -474,7 +474,7 @@ MXQ_API mxq_status mxq_kv_append(const mxq_norm_rope* cfg, const mxq_paged_kv* c
  * Softmax statistics and sums are FP32 (the tensor core's, which are cut and not rounded, over at most 2^16
  * keys: 0.03 % of a sum); the weights are rounded to the product's operand type (BF16;
  * FP16 with an E4M3 cache, by 2^-32 of the row's largest weight where that is more), the result once
- * to BF16.  With an E4M3 cache and more than 16 rows per key head the queries are exact down to 2^-9 of their
+ * to BF16.  With an E4M3 cache and more than 16 rows per key head (T * Hq / heads / batch) the queries are exact down to 2^-9 of their
  * row's largest value and off by at most 2^-17 of it below, and rows whose largest is under 2^-119
  * count as zeros (fewer rows: 2^-17, 2^-25, 2^-126).  Cached positions that no
  * row of a sequence attends may hold anything (NaN, Inf); a non-finite value of a key attended by
